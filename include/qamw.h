@@ -368,6 +368,76 @@ int qamw_decode_matmul(const uint32_t *packed, const float *row_norm, const floa
 size_t qamw_decode_matmul_workspace_bytes(int64_t M, int64_t K, int64_t T);
 
 /*
+ * Microscaled 4-bit floating point (OCP Microscaling Formats v1.0, MXFP4):
+ * e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with one
+ * power-of-two scale (e8m0) per group of 32 consecutive columns, 4.25 bits per
+ * weight, after the codec's own channel scale and block Hadamard rotation.
+ * The tensor cores multiply this form directly.
+ * (Interfaces of this library; the QAM-W page has no counterpart.)
+ *
+ *   v_j = w_j s_j (weights) or w_j / s_j (activations, divide != 0);
+ *   y   = H_b (d (.) v) / sqrt(b) per block of b columns (block == 0: y = v), both in fp64;
+ *   e   = clamp(floor(log2 max|y|) - 2, -127, 127) per group, scale byte e + 127;
+ *   q_j = the element nearest y_j 2^-e, ties to the even code, magnitudes above 6 to 6.
+ * An all-zero group has scale byte 0. A group that holds an Inf or NaN gets
+ * scale byte 255 (NaN) and codes 0, and sets QAMW_STATUS_NONFINITE_INPUT: it
+ * decodes to NaN and makes the products of its row NaN.
+ * Quantise W with s and X with the same s, block and seed and divide != 0:
+ * then x . w = y_x . y_w up to the 4-bit rounding, and the product of the two
+ * coded matrices needs no rotation and no scale.
+ *
+ * Layout: codes uint8 [M][K/2], the even column in the low half of a byte;
+ * scales uint8 [ceil(M/128)][ceil(K/128)][512], byte (r % 32) * 16 + (r / 32)
+ * * 4 + g of a tile for its row r and group g of 4 (the layout in which the
+ * tensor cores take scales; padding bytes are 0): qamw_mx4_scale_bytes(M, K)
+ * bytes. K is a multiple of 32; codes and scales are 16-byte aligned.
+ */
+#define QAMW_MX4_GROUP 32
+/* Bytes of the scales of an M x K matrix (0 if the shape is invalid). */
+size_t qamw_mx4_scale_bytes(int64_t M, int64_t K);
+
+/*
+ * qamw_mx4_quantize -- W (device [M][ldw] of w_dtype, unit column stride, any
+ * element alignment) to codes_out and scales_out.
+ *   col_scale: device float32 [K] (s_j) or NULL (s = 1)
+ *   block    : 0 (no rotation) or a power of two in [2, 1024] that divides K
+ * Errors: QAMW_ENULL, QAMW_EINVAL (shape, block, ldw, alignment), QAMW_EUNSUPPORTED.
+ */
+int qamw_mx4_quantize(const void *W, qamw_dtype w_dtype, int64_t M, int64_t K, int64_t ldw, const float *col_scale,
+                      int32_t divide, int32_t block, uint64_t sign_seed, uint8_t *codes_out, uint8_t *scales_out,
+                      int32_t *status, qamw_stream_t stream);
+
+/*
+ * qamw_mx4_decode -- the coded matrix in its original basis,
+ *   w_hat_j = d_j (H_b (q 2^e))_j / sqrt(b), divided by s_j (times s_j if divide != 0),
+ * fp32 arithmetic, rounded (RNE) to out_dtype. With block == 0 and col_scale
+ * == NULL it writes the values q 2^e themselves, exact in both types.
+ * Arguments as given to the quantisation; W_out: device [M][ldo].
+ */
+int qamw_mx4_decode(const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K, const float *col_scale,
+                    int32_t divide, int32_t block, uint64_t sign_seed, void *W_out, qamw_dtype out_dtype, int64_t ldo,
+                    qamw_stream_t stream);
+
+/*
+ * qamw_mx4_pack_scales / qamw_mx4_unpack_scales -- scale bytes between
+ * row-major uint8 [M][K/32] (the form of stored checkpoints) and the tiled
+ * layout above.
+ */
+int qamw_mx4_pack_scales(const uint8_t *rows, int64_t M, int64_t K, uint8_t *scales_out, qamw_stream_t stream);
+int qamw_mx4_unpack_scales(const uint8_t *scales, int64_t M, int64_t K, uint8_t *rows_out, qamw_stream_t stream);
+
+/*
+ * qamw_mx4_matmul -- Y[t][m] = sum_j x[t][j] w[m][j] for two coded matrices of
+ * the same K, on the block-scaled tensor cores (tcgen05 kind::mxf4): exact
+ * products, fp32 accumulation, one rounding to out_dtype. Y: device [T][ldy],
+ * written for t < T, m < M. A timed-out wait sets QAMW_STATUS_TIMEOUT.
+ * Errors: QAMW_ENULL, QAMW_EINVAL (shape, ldy, alignment), QAMW_EUNSUPPORTED.
+ */
+int qamw_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, const uint8_t *x_codes,
+                    const uint8_t *x_scales, int64_t T, int64_t K, void *Y, qamw_dtype out_dtype, int64_t ldy,
+                    int32_t *status, qamw_stream_t stream);
+
+/*
  * qamw_rotate_rows -- the rotation alone, for tests of step (2).
  * inverse == 0: Y = H_b (d * U) / sqrt(b); inverse != 0: Y = d * (H_b U) / sqrt(b),
  * per block of b columns, in fp64 (the encode path's arithmetic).

@@ -15,6 +15,7 @@ Module map:
                 nearest centroid (with tie gaps), bit packing, decode.
   lloyd      -- joint 2D Lloyd-Max codebook training on unit circular Gaussian
                 samples, and the polar amplitude/phase baseline code.
+  mx4        -- microscaled 4-bit floating point: quantisation, values, decode.
   make_codebooks -- script that trains and writes the shipped codebook tables.
 
 Pins: every function is checked in ``tests/test_oracle_*.py`` against facts
@@ -24,4 +25,4 @@ the trace identity, exact rational brute force, known bit patterns). The
 whole-pipeline composition beyond those pins is "parity unpinned": the pages
 print no worked numeric example.
 """
-from . import codec, lloyd  # noqa: F401
+from . import codec, lloyd, mx4  # noqa: F401

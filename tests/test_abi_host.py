@@ -263,3 +263,60 @@ def test_decode_matmul_rejects_on_host(lib):
     assert call(K=192, block=64, ldx=192) == QAMW_EUNSUPPORTED          # K not a multiple of 128
     big = lib.qamw_decode_matmul_workspace_bytes(128, 32768 + 128, 16)
     assert call(K=32768 + 128, ldx=32768 + 128, nws=big) == QAMW_EUNSUPPORTED
+
+
+def test_mx4_scale_bytes(lib):
+    """Tiles of 128 rows x 128 columns, 512 bytes each; 0 for an invalid shape."""
+    assert lib.qamw_mx4_scale_bytes(1, 32) == 512
+    assert lib.qamw_mx4_scale_bytes(129, 160) == 4 * 512
+    assert lib.qamw_mx4_scale_bytes(11008, 4096) == 86 * 32 * 512
+    for M, K in ((0, 32), (1, 0), (1, 31), (1, 48), (1 << 31, 32)):
+        assert lib.qamw_mx4_scale_bytes(M, K) == 0
+
+
+def _mxq(lib, **kw):
+    a = dict(W=FAKE, wt=1, M=8, K=256, ldw=256, s=None, divide=0, block=128, seed=1, codes=FAKE, scales=FAKE)
+    a.update(kw)
+    return lib.qamw_mx4_quantize(*a.values(), None, None)
+
+
+def _mxd(lib, **kw):
+    a = dict(codes=FAKE, scales=FAKE, M=8, K=256, s=None, divide=0, block=128, seed=1, out=FAKE, ot=1, ldo=256)
+    a.update(kw)
+    return lib.qamw_mx4_decode(*a.values(), None)
+
+
+def _mxm(lib, **kw):
+    a = dict(wc=FAKE, ws=FAKE, M=8, xc=FAKE, xs=FAKE, T=4, K=256, Y=FAKE, ot=0, ldy=8)
+    a.update(kw)
+    return lib.qamw_mx4_matmul(*a.values(), None, None)
+
+
+ODD = ctypes.c_void_p(0x10001)
+
+
+@pytest.mark.parametrize("call,kw,rc", [
+    (_mxq, dict(W=None), QAMW_ENULL), (_mxq, dict(codes=None), QAMW_ENULL), (_mxq, dict(scales=None), QAMW_ENULL),
+    (_mxq, dict(wt=7), QAMW_EINVAL), (_mxq, dict(M=0), QAMW_EINVAL), (_mxq, dict(K=240), QAMW_EINVAL),
+    (_mxq, dict(K=0), QAMW_EINVAL), (_mxq, dict(ldw=255), QAMW_EINVAL), (_mxq, dict(block=1), QAMW_EINVAL),
+    (_mxq, dict(block=96), QAMW_EINVAL), (_mxq, dict(block=512), QAMW_EINVAL),
+    (_mxq, dict(block=2048, K=2048, ldw=2048), QAMW_EUNSUPPORTED), (_mxq, dict(W=ODD), QAMW_EINVAL),
+    (_mxq, dict(codes=ODD), QAMW_EINVAL), (_mxq, dict(M=(1 << 30) + 1), QAMW_EUNSUPPORTED),
+    (_mxd, dict(codes=None), QAMW_ENULL), (_mxd, dict(out=None), QAMW_ENULL), (_mxd, dict(ot=9), QAMW_EINVAL),
+    (_mxd, dict(ldo=200), QAMW_EINVAL), (_mxd, dict(block=-2), QAMW_EINVAL), (_mxd, dict(scales=ODD), QAMW_EINVAL),
+    (_mxd, dict(out=ODD), QAMW_EINVAL),
+    (_mxm, dict(wc=None), QAMW_ENULL), (_mxm, dict(xs=None), QAMW_ENULL), (_mxm, dict(Y=None), QAMW_ENULL),
+    (_mxm, dict(T=0), QAMW_EINVAL), (_mxm, dict(ldy=7), QAMW_EINVAL), (_mxm, dict(ot=2), QAMW_EINVAL),
+    (_mxm, dict(K=100), QAMW_EINVAL), (_mxm, dict(xc=ODD), QAMW_EINVAL),
+])
+def test_mx4_rejects_bad_arguments(lib, call, kw, rc):
+    assert call(lib, **kw) == rc
+    assert lib.qamw_last_error()
+
+
+def test_mx4_scale_layout_rejects_bad_arguments(lib):
+    for f in (lib.qamw_mx4_pack_scales, lib.qamw_mx4_unpack_scales):
+        assert f(None, 4, 64, FAKE, None) == QAMW_ENULL
+        assert f(FAKE, 4, 64, None, None) == QAMW_ENULL
+        assert f(FAKE, 4, 65, FAKE, None) == QAMW_EINVAL
+        assert f(FAKE, 0, 64, FAKE, None) == QAMW_EINVAL

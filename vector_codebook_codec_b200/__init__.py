@@ -17,6 +17,7 @@ tensors.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import json
 import os
@@ -69,6 +70,15 @@ _SIGNATURES = {
     "qamw_calibrate_partial_sums": (ctypes.c_int, [_c_p, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_f32,
                                                    _c_i32, _c_u64, _c_p, _c_p, _c_sz, _c_p, _c_p]),
     "qamw_sigma_from_partial_sums": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_p, _c_p]),
+    "qamw_mx4_scale_bytes": (_c_sz, [_c_i64, _c_i64]),
+    "qamw_mx4_quantize": (ctypes.c_int, [_c_p, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_i32, _c_i32, _c_u64,
+                                         _c_p, _c_p, _c_p, _c_p]),
+    "qamw_mx4_decode": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_i32, _c_i32, _c_u64, _c_p, ctypes.c_int,
+                                       _c_i64, _c_p]),
+    "qamw_mx4_pack_scales": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p]),
+    "qamw_mx4_unpack_scales": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p]),
+    "qamw_mx4_matmul": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_p, ctypes.c_int, _c_i64,
+                                       _c_p, _c_p]),
     "qamw_lloyd_workspace_bytes": (_c_sz, [_c_i64, _c_i32]),
     "qamw_lloyd_assign": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_p]),
     "qamw_lloyd_update": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_sz, _c_p]),
@@ -144,6 +154,12 @@ qamw_encode_prepared = _raw("qamw_encode_prepared")
 qamw_search_cells = _raw("qamw_search_cells")
 qamw_decode_matmul = _raw("qamw_decode_matmul")
 qamw_decode_matmul_workspace_bytes = _raw("qamw_decode_matmul_workspace_bytes")
+qamw_mx4_scale_bytes = _raw("qamw_mx4_scale_bytes")
+qamw_mx4_quantize = _raw("qamw_mx4_quantize")
+qamw_mx4_decode = _raw("qamw_mx4_decode")
+qamw_mx4_pack_scales = _raw("qamw_mx4_pack_scales")
+qamw_mx4_unpack_scales = _raw("qamw_mx4_unpack_scales")
+qamw_mx4_matmul = _raw("qamw_mx4_matmul")
 
 
 # ---------------------------------------------------------------------------
@@ -473,6 +489,221 @@ def decode_matmul(enc: Encoded, codebook, X, status=None, stream=None, out=None,
         _ptr(Y), _ld(Y), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
         _stream_ptr(stream)))
     return Y
+
+
+# ---------------------------------------------------------------------------
+# microscaled 4-bit floating point (qamw_mx4_*)
+# ---------------------------------------------------------------------------
+
+@dataclass
+class Mx4:
+    """A matrix in microscaled 4-bit form: e2m1 codes and e8m0 scales, and how its rows were prepared."""
+    codes: object       # uint8 [M, K/2], the even column in the low half
+    scales: object      # uint8 [qamw_mx4_scale_bytes(M, K)], tiled
+    M: int
+    K: int
+    block: int          # 0: no rotation
+    seed: int
+    col_scale: object   # float32 [K] or None (s = 1)
+    divide: bool        # the rows were divided by s (activations) instead of multiplied (weights)
+
+
+@contextlib.contextmanager
+def _on(first, stream):
+    """The device of ``first``, and ``stream`` as its current stream, so that
+    what a call allocates for itself belongs to the stream that uses it."""
+    torch = _torch()
+    with torch.cuda.device(first.device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _same_device(first, **tensors):
+    """Every tensor given lies on the device of `first`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+
+
+def _need_out(name, out, shape, dtype):
+    """A caller's output: right shape and type, unit column stride, rows apart."""
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    if out.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {out.dtype}")
+    if out.dim() == 2 and out.shape[0] > 1 and out.stride(0) < out.shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows")
+
+
+def _need_status(first, status):
+    torch = _torch()
+    _need_cuda("status", status, torch.int32)
+    _same_device(first, status=status)
+    if status is not None and status.numel() < 1:
+        raise ValueError("status must hold one int32")
+
+
+def _need_scale(first, col_scale, K):
+    torch = _torch()
+    _need_cuda("col_scale", col_scale, torch.float32, 1)
+    _same_device(first, col_scale=col_scale)
+    if col_scale is not None and (col_scale.shape[0] != K or (K > 1 and col_scale.stride(0) != 1)):
+        raise ValueError("col_scale must be K contiguous values")
+
+
+def _need_mx4(name, q):
+    """The tensors of an Mx4 agree with its shape (the kernels trust them)."""
+    torch = _torch()
+    _need_cuda(f"{name}.codes", q.codes, torch.uint8, 2)
+    _need_cuda(f"{name}.scales", q.scales, torch.uint8, 1)
+    _same_device(q.codes, **{f"{name}.scales": q.scales})
+    if tuple(q.codes.shape) != (q.M, q.K // 2) or not q.codes.is_contiguous():
+        raise ValueError(f"{name}.codes must be contiguous [M, K/2]")
+    if q.scales.numel() != mx4_scale_bytes(q.M, q.K) or not q.scales.is_contiguous():
+        raise ValueError(f"{name}.scales must be qamw_mx4_scale_bytes(M, K) contiguous bytes")
+    _need_scale(q.codes, q.col_scale, q.K)
+
+
+def _out_type(out_dtype):
+    torch = _torch()
+    if out_dtype == torch.bfloat16:
+        return QAMW_BF16
+    if out_dtype == torch.float32:
+        return QAMW_F32
+    raise ValueError("out_dtype must be bfloat16 or float32")
+
+
+def mx4_scale_bytes(M: int, K: int) -> int:
+    n = int(load_library().qamw_mx4_scale_bytes(M, K))
+    if n == 0:
+        raise ValueError(f"no microscaled form of a {M} x {K} matrix (K must be a multiple of 32)")
+    return n
+
+
+def mx4_quantize(W, block: int = 0, seed: int = 0, col_scale=None, divide: bool = False, status=None, stream=None,
+                 out=None) -> Mx4:
+    """W (bf16 or fp32 CUDA tensor [M, K], unit column stride) in microscaled
+    4-bit form (qamw_mx4_quantize): columns times ``col_scale`` (divided by it
+    with ``divide``, the activations' side of a product), the sign-masked block
+    Hadamard rotation (``block`` 0: none), e2m1 codes with one e8m0 scale per
+    32 columns. ``out`` = (codes, scales) preallocated, or None."""
+    torch = _torch()
+    _need_cuda("W", W, ndim=2)
+    wt, ld = _wdtype(W), _ld(W)
+    M, K = W.shape
+    n_scales = mx4_scale_bytes(M, K)
+    _need_scale(W, col_scale, K)
+    _need_status(W, status)
+    with _on(W, stream):
+        if out is None:
+            codes = torch.empty((M, K // 2), dtype=torch.uint8, device=W.device)
+            scales = torch.empty(n_scales, dtype=torch.uint8, device=W.device)
+        else:
+            codes, scales = out
+        q = Mx4(codes, scales, M, K, block, seed, col_scale, bool(divide))
+        _need_mx4("out", q)
+        _same_device(W, out=codes)
+        _check("qamw_mx4_quantize", load_library().qamw_mx4_quantize(
+            _ptr(W), wt, M, K, ld, _ptr(col_scale), int(q.divide), block, seed & (2**64 - 1), _ptr(codes),
+            _ptr(scales), _ptr(status), _stream_ptr(stream)))
+    return q
+
+
+def mx4_decode(q: Mx4, out_dtype=None, original: bool = True, stream=None, out=None):
+    """The matrix that ``q`` stands for, bf16 (default) or fp32 [M, K], in its
+    original basis (qamw_mx4_decode); ``original`` False gives the coded values
+    themselves (rotated and scaled as they were quantised), exact in both types."""
+    torch = _torch()
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    ot = _out_type(out_dtype)
+    _need_mx4("q", q)
+    with _on(q.codes, stream):
+        if out is None:
+            out = torch.empty((q.M, q.K), dtype=out_dtype, device=q.codes.device)
+        _need_cuda("out", out, ndim=2)
+        _need_out("out", out, (q.M, q.K), out_dtype)
+        _same_device(q.codes, out=out)
+        _check("qamw_mx4_decode", load_library().qamw_mx4_decode(
+            _ptr(q.codes), _ptr(q.scales), q.M, q.K, _ptr(q.col_scale) if original else None, int(q.divide),
+            q.block if original else 0, q.seed & (2**64 - 1), _ptr(out), ot, _ld(out), _stream_ptr(stream)))
+    return out
+
+
+def mx4_from_parts(codes, scale_rows, block: int = 0, seed: int = 0, col_scale=None, divide: bool = False,
+                   stream=None) -> Mx4:
+    """An :class:`Mx4` from a checkpoint's tensors: codes uint8 [M, K/2] (the
+    even column in the low half) and e8m0 scale bytes uint8 [M, K/32]. The
+    codes are taken as they are, the scales laid out for the tensor cores."""
+    torch = _torch()
+    _need_cuda("codes", codes, torch.uint8, 2)
+    _need_cuda("scale_rows", scale_rows, torch.uint8, 2)
+    _same_device(codes, scale_rows=scale_rows)
+    M, K = codes.shape[0], 2 * codes.shape[1]
+    if tuple(scale_rows.shape) != (M, K // 32):
+        raise ValueError(f"scale_rows must be [{M}, {K // 32}]")
+    with _on(codes, stream):
+        codes, scale_rows = codes.contiguous(), scale_rows.contiguous()
+        scales = torch.empty(mx4_scale_bytes(M, K), dtype=torch.uint8, device=codes.device)
+        _check("qamw_mx4_pack_scales", load_library().qamw_mx4_pack_scales(
+            _ptr(scale_rows), M, K, _ptr(scales), _stream_ptr(stream)))
+    q = Mx4(codes, scales, M, K, block, seed, col_scale, bool(divide))
+    _need_mx4("q", q)
+    return q
+
+
+def mx4_scale_rows(q: Mx4, stream=None):
+    """The e8m0 scale bytes of ``q``, row-major (uint8 [M, K/32])."""
+    torch = _torch()
+    _need_mx4("q", q)
+    with _on(q.codes, stream):
+        rows = torch.empty((q.M, q.K // 32), dtype=torch.uint8, device=q.codes.device)
+        _check("qamw_mx4_unpack_scales", load_library().qamw_mx4_unpack_scales(
+            _ptr(q.scales), q.M, q.K, _ptr(rows), _stream_ptr(stream)))
+    return rows
+
+
+def mx4_matmul(W: Mx4, X: Mx4, out_dtype=None, status=None, stream=None, out=None):
+    """Y [T, M] = X W^T of two microscaled matrices (qamw_mx4_matmul), fp32
+    (default) or bf16. Both must be rotated alike; a channel scale on one side
+    must be divided out on the other (:func:`mx4_linear` does that)."""
+    torch = _torch()
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    ot = _out_type(out_dtype)
+    _need_mx4("W", W)
+    _need_mx4("X", X)
+    _same_device(W.codes, X=X.codes)
+    _need_status(W.codes, status)
+    if W.K != X.K:
+        raise ValueError(f"W has {W.K} columns and X {X.K}")
+    if (W.block, W.seed & (2**64 - 1) if W.block else 0) != (X.block, X.seed & (2**64 - 1) if X.block else 0):
+        raise ValueError("W and X must be rotated with the same block and seed")
+    with _on(W.codes, stream):
+        if out is None:
+            out = torch.empty((X.M, W.M), dtype=out_dtype, device=W.codes.device)
+        _need_cuda("out", out, ndim=2)
+        _need_out("out", out, (X.M, W.M), out_dtype)
+        _same_device(W.codes, out=out)
+        _check("qamw_mx4_matmul", load_library().qamw_mx4_matmul(
+            _ptr(W.codes), _ptr(W.scales), W.M, _ptr(X.codes), _ptr(X.scales), X.M, W.K, _ptr(out), ot, _ld(out),
+            _ptr(status), _stream_ptr(stream)))
+    return out
+
+
+def mx4_linear(W: Mx4, X, out_dtype=None, status=None, stream=None, out=None):
+    """Y [T, M] = X W^T for a microscaled weight matrix and bf16 or fp32
+    activations X [T, K]: X is quantised as W was (the same rotation, the
+    channel scale divided out), then multiplied on the tensor cores."""
+    if W.divide:
+        raise ValueError("W was quantised with divide=True: it is the activations' side of a product")
+    _need_cuda("X", X, ndim=2)
+    if X.shape[1] != W.K:
+        raise ValueError("X must have K columns")
+    with _on(W.codes, stream):
+        Xq = mx4_quantize(X, W.block, W.seed, W.col_scale, divide=True, status=status)
+        return mx4_matmul(W, Xq, out_dtype, status=status, out=out)
 
 
 def rotate_rows(U, block: int, seed: int, inverse: bool = False, stream=None):

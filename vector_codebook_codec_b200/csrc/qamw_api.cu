@@ -621,6 +621,118 @@ int qamw_lloyd_train(const double *points, int64_t T, double *centroids, int32_t
   return QAMW_OK;
 }
 
+// Shape checks of the microscaled 4-bit entry points.
+static int check_mx4(int64_t M, int64_t K, const char *fn) {
+  if (M < 1) return fail(QAMW_EINVAL, "%s: the number of rows must be >= 1 (got %lld)", fn, (long long)M);
+  if (K < QAMW_MX4_GROUP || K % QAMW_MX4_GROUP)
+    return fail(QAMW_EINVAL, "%s: K must be a positive multiple of %d (got %lld)", fn, QAMW_MX4_GROUP, (long long)K);
+  if (M > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return fail(QAMW_EUNSUPPORTED, "%s: shape too large", fn);
+  return QAMW_OK;
+}
+
+static int check_mx4_block(int64_t K, int32_t block, const char *fn) {
+  if (block == 0) return QAMW_OK;
+  if (!is_pow2(block) || block < 2)
+    return fail(QAMW_EINVAL, "%s: block must be 0 or a power of two >= 2 (got %d)", fn, block);
+  if (block > QAMW_MAX_BLOCK) return fail(QAMW_EUNSUPPORTED, "%s: block %d exceeds %d", fn, block, QAMW_MAX_BLOCK);
+  if (K % block) return fail(QAMW_EINVAL, "%s: K (%lld) must be a multiple of block (%d)", fn, (long long)K, block);
+  return QAMW_OK;
+}
+
+static int check_mx4_codes(const void *codes, const void *scales, const char *fn) {
+  if (!codes || !scales) return fail(QAMW_ENULL, "%s: codes and scales must be non-NULL", fn);
+  if (reinterpret_cast<uintptr_t>(codes) % 16 || reinterpret_cast<uintptr_t>(scales) % 16)
+    return fail(QAMW_EINVAL, "%s: codes and scales must be 16-byte aligned", fn);
+  return QAMW_OK;
+}
+
+static bool element_aligned(const void *p, qamw_dtype t) {
+  return reinterpret_cast<uintptr_t>(p) % (t == QAMW_BF16 ? 2 : 4) == 0;
+}
+
+size_t qamw_mx4_scale_bytes(int64_t M, int64_t K) {
+  if (M < 1 || K < QAMW_MX4_GROUP || K % QAMW_MX4_GROUP || M > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return 0;
+  return mx4_scale_bytes(M, K);
+}
+
+int qamw_mx4_quantize(const void *W, qamw_dtype w_dtype, int64_t M, int64_t K, int64_t ldw, const float *col_scale,
+                      int32_t divide, int32_t block, uint64_t sign_seed, uint8_t *codes_out, uint8_t *scales_out,
+                      int32_t *status, qamw_stream_t stream) {
+  static const char *fn = "qamw_mx4_quantize";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  if (!W) return fail(QAMW_ENULL, "%s: W must be non-NULL", fn);
+  if ((rc = check_dtype(w_dtype, fn))) return rc;
+  if ((rc = check_mx4(M, K, fn))) return rc;
+  if ((rc = check_mx4_block(K, block, fn))) return rc;
+  if ((rc = check_mx4_codes(codes_out, scales_out, fn))) return rc;
+  if (ldw < K) return fail(QAMW_EINVAL, "%s: ldw (%lld) < K (%lld)", fn, (long long)ldw, (long long)K);
+  if (!element_aligned(W, w_dtype)) return fail(QAMW_EINVAL, "%s: W must be aligned to its element size", fn);
+  Mx4QuantizeArgs a{W, w_dtype, M, K, ldw, col_scale, divide, block ? log2i(block) : 0, sign_seed, codes_out,
+                    scales_out, status};
+  cudaError_t e = launch_mx4_quantize(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
+int qamw_mx4_decode(const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K, const float *col_scale,
+                    int32_t divide, int32_t block, uint64_t sign_seed, void *W_out, qamw_dtype out_dtype, int64_t ldo,
+                    qamw_stream_t stream) {
+  static const char *fn = "qamw_mx4_decode";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  if (!W_out) return fail(QAMW_ENULL, "%s: W_out must be non-NULL", fn);
+  if ((rc = check_dtype(out_dtype, fn))) return rc;
+  if ((rc = check_mx4(M, K, fn))) return rc;
+  if ((rc = check_mx4_block(K, block, fn))) return rc;
+  if ((rc = check_mx4_codes(codes, scales, fn))) return rc;
+  if (ldo < K) return fail(QAMW_EINVAL, "%s: ldo (%lld) < K (%lld)", fn, (long long)ldo, (long long)K);
+  if (!element_aligned(W_out, out_dtype)) return fail(QAMW_EINVAL, "%s: W_out must be aligned to its element size", fn);
+  Mx4DecodeArgs a{codes, scales, M, K, col_scale, divide, block ? log2i(block) : 0, sign_seed, W_out, out_dtype, ldo};
+  cudaError_t e = launch_mx4_decode(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
+static int mx4_scale_layout(const uint8_t *in, uint8_t *out, int64_t M, int64_t K, bool to_tiles, qamw_stream_t stream,
+                            const char *fn) {
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  if (!in || !out) return fail(QAMW_ENULL, "%s: the scales and the output must be non-NULL", fn);
+  if ((rc = check_mx4(M, K, fn))) return rc;
+  cudaError_t e = launch_mx4_scale_layout(in, out, M, K, to_tiles, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
+int qamw_mx4_pack_scales(const uint8_t *rows, int64_t M, int64_t K, uint8_t *scales_out, qamw_stream_t stream) {
+  return mx4_scale_layout(rows, scales_out, M, K, true, stream, "qamw_mx4_pack_scales");
+}
+
+int qamw_mx4_unpack_scales(const uint8_t *scales, int64_t M, int64_t K, uint8_t *rows_out, qamw_stream_t stream) {
+  return mx4_scale_layout(scales, rows_out, M, K, false, stream, "qamw_mx4_unpack_scales");
+}
+
+int qamw_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, const uint8_t *x_codes,
+                    const uint8_t *x_scales, int64_t T, int64_t K, void *Y, qamw_dtype out_dtype, int64_t ldy,
+                    int32_t *status, qamw_stream_t stream) {
+  static const char *fn = "qamw_mx4_matmul";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  if (!Y) return fail(QAMW_ENULL, "%s: Y must be non-NULL", fn);
+  if ((rc = check_dtype(out_dtype, fn))) return rc;
+  if ((rc = check_mx4(M, K, fn))) return rc;
+  if ((rc = check_mx4(T, K, fn))) return rc;
+  if ((rc = check_mx4_codes(w_codes, w_scales, fn))) return rc;
+  if ((rc = check_mx4_codes(x_codes, x_scales, fn))) return rc;
+  if (ldy < M) return fail(QAMW_EINVAL, "%s: ldy (%lld) < M (%lld)", fn, (long long)ldy, (long long)M);
+  if (!element_aligned(Y, out_dtype)) return fail(QAMW_EINVAL, "%s: Y must be aligned to its element size", fn);
+  Mx4MatmulArgs a{w_codes, w_scales, M, x_codes, x_scales, T, K, Y, out_dtype, ldy, status};
+  cudaError_t e = launch_mx4_matmul(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
 int qamw_selftest_wait_timeout(uint32_t tries, int32_t *status, qamw_stream_t stream) {
   static const char *fn = "qamw_selftest_wait_timeout";
   CallRange nvtx_range(fn);

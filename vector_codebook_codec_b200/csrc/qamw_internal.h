@@ -174,6 +174,50 @@ cudaError_t launch_decode_gemm(const DecodeArgs &d, const uint16_t *X, int64_t T
 // The same for b <= 512 with the 512-column rotation of the encode and calibrate kernels.
 cudaError_t launch_rotate_test512(const RotateTestArgs &a, cudaStream_t s);
 
+// Microscaled 4-bit floating point (qamw_mx4.cu): codes [M][K/2], scales in
+// tiles of 128 rows x 4 groups of 32 columns (mx4_scale_bytes).
+struct Mx4QuantizeArgs {
+  const void *W;
+  qamw_dtype wt;
+  int64_t M, K, ldw;
+  const float *col_scale;  // nullable
+  int32_t divide;          // v = w / s instead of w * s
+  int32_t log2b;           // 0: no rotation
+  uint64_t seed;
+  uint8_t *codes, *scales;
+  int32_t *status;
+};
+struct Mx4DecodeArgs {
+  const uint8_t *codes, *scales;
+  int64_t M, K;
+  const float *col_scale;  // nullable
+  int32_t divide;          // as given to the quantisation
+  int32_t log2b;
+  uint64_t seed;
+  void *out;
+  qamw_dtype out_t;
+  int64_t ldo;
+};
+inline size_t mx4_scale_bytes(int64_t M, int64_t K) {
+  return (size_t)((M + 127) / 128) * (size_t)((K + 127) / 128) * 512;
+}
+cudaError_t launch_mx4_quantize(const Mx4QuantizeArgs &a, cudaStream_t s);
+cudaError_t launch_mx4_decode(const Mx4DecodeArgs &a, cudaStream_t s);
+cudaError_t launch_mx4_scale_layout(const uint8_t *in, uint8_t *out, int64_t M, int64_t K, bool to_tiles,
+                                    cudaStream_t s);
+// Y[t][m] = sum_j x[t][j] w[m][j] of two coded matrices (qamw_mx4_gemm.cu).
+struct Mx4MatmulArgs {
+  const uint8_t *w_codes, *w_scales;
+  int64_t M;
+  const uint8_t *x_codes, *x_scales;
+  int64_t T, K;
+  void *Y;
+  qamw_dtype out_t;
+  int64_t ldy;
+  int32_t *status;
+};
+cudaError_t launch_mx4_matmul(const Mx4MatmulArgs &a, cudaStream_t s);
+
 // Lloyd training of the 2D codebook (qamw_lloyd.cu); points and centroids are
 // fp64 [.][2], 16-byte aligned.
 size_t lloyd_workspace_bytes(int64_t T, int N);
