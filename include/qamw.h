@@ -438,6 +438,62 @@ int qamw_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, 
                     int32_t *status, qamw_stream_t stream);
 
 /*
+ * Softmax cross entropy of a model's head, without keeping the logits, and its
+ * gradient -- the quantity by which the pages judge a coded model (its
+ * perplexity is exp of the mean loss).
+ * (Interfaces of this library; the QAM-W page has no counterpart.)
+ *   l_tv = sum_j X_tj W_vj;  lse_t = log sum_v exp l_tv;  loss_t = lse_t - l_t,target(t)
+ *   G_tv = g_t (exp(l_tv - lse_t) - [v = target(t)]);  dX = G W;  dW = G^T X
+ * The vocabulary is worked through in pieces, so that a coded head is decoded
+ * a piece at a time and neither the logits nor G of the whole vocabulary exist:
+ * entries v0 .. v0 + n - 1 are the rows of W given in the call. Pieces start at
+ * multiples of QAMW_VOCAB_TILE and, but for the last, hold multiples of it;
+ * every entry belongs to exactly one piece. A token whose target is
+ * ignore_index has loss 0 and no part in the gradients; any other target
+ * outside [0, V) is treated alike and sets QAMW_STATUS_BAD_INDEX.
+ *   X : device bf16 [T][ldx]    W : device bf16 [n][ldw]   (16-byte aligned,
+ *       ldx and ldw multiples of 8; K a multiple of 8, T at most 2^24)
+ *   targets : device int64 [T]  workspace : device, 256-byte aligned
+ * Products of bf16 values with fp32 accumulation (tcgen05), softmax statistics
+ * in fp32. A timed-out wait sets QAMW_STATUS_TIMEOUT.
+ *
+ * Forward: qamw_cross_entropy_piece for every piece (in any order, one
+ * stream), then qamw_cross_entropy_finish writes loss and lse (device float32
+ * [T]). The workspace is qamw_cross_entropy_workspace_bytes(T, V) bytes: a
+ * maximum and a sum per token and 256 entries, combined in a fixed order.
+ *
+ * Backward: qamw_cross_entropy_grad_piece for every piece, one after another
+ * (`first` != 0 for the first of them, `piece` the same in all calls and at
+ * least every n), then qamw_cross_entropy_grad_finish writes dX (device bf16
+ * [T][lddx]).
+ *   lse : from the forward pass   grad_loss : device float32 [T], g_t = dL/dloss_t
+ *   dW  : device bf16 [n][lddw], this piece's rows, or NULL (a frozen head)
+ * G of a piece is rounded to bf16 (2^-8 relative at most) for the two products;
+ * dX is summed over pieces and splits in fp32 in a fixed order and rounded once,
+ * dW is rounded once. Rows of X whose token is ignored are not read into dW:
+ * they may hold anything. Workspace: qamw_cross_entropy_grad_workspace_bytes(T,
+ * K, piece) bytes (G of one piece, X without its ignored rows, the fp32 terms
+ * of dX).
+ * Errors: QAMW_ENULL, QAMW_EINVAL (sizes, piece, alignment), QAMW_EWORKSPACE,
+ * QAMW_EUNSUPPORTED.
+ */
+#define QAMW_VOCAB_TILE 256
+size_t qamw_cross_entropy_workspace_bytes(int64_t T, int64_t V);
+int qamw_cross_entropy_piece(const void *X, int64_t T, int64_t K, int64_t ldx, const void *W, int64_t n, int64_t ldw,
+                             int64_t v0, int64_t V, const int64_t *targets, int64_t ignore_index, void *workspace,
+                             size_t workspace_bytes, int32_t *status, qamw_stream_t stream);
+int qamw_cross_entropy_finish(int64_t T, int64_t V, const int64_t *targets, int64_t ignore_index, void *workspace,
+                              size_t workspace_bytes, float *loss, float *lse, int32_t *status, qamw_stream_t stream);
+size_t qamw_cross_entropy_grad_workspace_bytes(int64_t T, int64_t K, int64_t piece);
+int qamw_cross_entropy_grad_piece(const void *X, int64_t T, int64_t K, int64_t ldx, const void *W, int64_t n,
+                                  int64_t ldw, int64_t v0, int64_t V, const int64_t *targets, int64_t ignore_index,
+                                  const float *lse, const float *grad_loss, int64_t piece, int32_t first, void *dW,
+                                  int64_t lddw, void *workspace, size_t workspace_bytes, int32_t *status,
+                                  qamw_stream_t stream);
+int qamw_cross_entropy_grad_finish(int64_t T, int64_t K, int64_t piece, void *dX, int64_t lddx, void *workspace,
+                                   size_t workspace_bytes, qamw_stream_t stream);
+
+/*
  * qamw_rotate_rows -- the rotation alone, for tests of step (2).
  * inverse == 0: Y = H_b (d * U) / sqrt(b); inverse != 0: Y = d * (H_b U) / sqrt(b),
  * per block of b columns, in fp64 (the encode path's arithmetic).

@@ -320,3 +320,72 @@ def test_mx4_scale_layout_rejects_bad_arguments(lib):
         assert f(FAKE, 4, 64, None, None) == QAMW_ENULL
         assert f(FAKE, 4, 65, FAKE, None) == QAMW_EINVAL
         assert f(FAKE, 0, 64, FAKE, None) == QAMW_EINVAL
+
+
+def test_cross_entropy_workspace_bytes(lib):
+    """A maximum and a sum per token and 256 entries, then a logit per token."""
+    def a256(n):
+        return (n + 255) // 256 * 256
+    for T, V in ((1, 1), (300, 50021), (4096, 65536)):
+        assert lib.qamw_cross_entropy_workspace_bytes(T, V) == a256(8 * T * ((V + 255) // 256)) + a256(4 * T)
+    for T, V in ((0, 5), (5, 0), ((1 << 24) + 1, 5)):
+        assert lib.qamw_cross_entropy_workspace_bytes(T, V) == 0
+    assert lib.qamw_cross_entropy_grad_workspace_bytes(4, 8, 256) >= 4 * 256 * 2 + 4 * 8 * 6
+    for T, K, p in ((0, 8, 256), (4, 12, 256), (4, 8, 0)):
+        assert lib.qamw_cross_entropy_grad_workspace_bytes(T, K, p) == 0
+
+
+BIG = 1 << 40
+
+
+def _cep(lib, **kw):
+    a = dict(X=FAKE, T=8, K=64, ldx=64, W=FAKE, n=300, ldw=64, v0=0, V=300, t=FAKE, ignore=-100, ws=FAKE, wb=BIG)
+    a.update(kw)
+    return lib.qamw_cross_entropy_piece(*a.values(), None, None)
+
+
+def _cef(lib, **kw):
+    a = dict(T=8, V=300, t=FAKE, ignore=-100, ws=FAKE, wb=BIG, loss=FAKE, lse=FAKE)
+    a.update(kw)
+    return lib.qamw_cross_entropy_finish(*a.values(), None, None)
+
+
+def _ceg(lib, **kw):
+    a = dict(X=FAKE, T=8, K=64, ldx=64, W=FAKE, n=300, ldw=64, v0=0, V=300, t=FAKE, ignore=-100, lse=FAKE, g=FAKE,
+             piece=300, first=1, dW=None, lddw=0, ws=FAKE, wb=BIG)
+    a.update(kw)
+    return lib.qamw_cross_entropy_grad_piece(*a.values(), None, None)
+
+
+def _cex(lib, **kw):
+    a = dict(T=8, K=64, piece=300, dX=FAKE, lddx=64, ws=FAKE, wb=BIG)
+    a.update(kw)
+    return lib.qamw_cross_entropy_grad_finish(*a.values(), None)
+
+
+@pytest.mark.parametrize("call", [_cep, _ceg])
+@pytest.mark.parametrize("kw,rc", [
+    (dict(X=None), QAMW_ENULL), (dict(W=None), QAMW_ENULL), (dict(t=None), QAMW_ENULL), (dict(T=0), QAMW_EINVAL),
+    (dict(T=(1 << 24) + 1), QAMW_EINVAL), (dict(K=60), QAMW_EINVAL), (dict(ldx=60), QAMW_EINVAL),
+    (dict(ldx=68), QAMW_EINVAL), (dict(ldw=56), QAMW_EINVAL), (dict(v0=100, V=1000), QAMW_EINVAL),
+    (dict(v0=256), QAMW_EINVAL), (dict(n=300, V=1000), QAMW_EINVAL), (dict(n=0), QAMW_EINVAL),
+    (dict(v0=-256), QAMW_EINVAL), (dict(X=ODD), QAMW_EINVAL), (dict(W=ODD), QAMW_EINVAL), (dict(t=ODD), QAMW_EINVAL),
+    (dict(ws=None), QAMW_EWORKSPACE), (dict(wb=100), QAMW_EWORKSPACE), (dict(ws=ODD), QAMW_EINVAL),
+    (dict(V=1 << 31, n=256), QAMW_EUNSUPPORTED),
+])
+def test_cross_entropy_pieces_reject_bad_arguments(lib, call, kw, rc):
+    assert call(lib, **kw) == rc
+    assert lib.qamw_last_error()
+
+
+@pytest.mark.parametrize("call,kw,rc", [
+    (_cef, dict(t=None), QAMW_ENULL), (_cef, dict(loss=None), QAMW_ENULL), (_cef, dict(lse=None), QAMW_ENULL),
+    (_cef, dict(T=0), QAMW_EINVAL), (_cef, dict(V=0), QAMW_EINVAL), (_cef, dict(wb=16), QAMW_EWORKSPACE),
+    (_ceg, dict(lse=None), QAMW_ENULL), (_ceg, dict(g=None), QAMW_ENULL), (_ceg, dict(piece=299), QAMW_EINVAL),
+    (_ceg, dict(dW=FAKE, lddw=63), QAMW_EINVAL), (_ceg, dict(dW=ODD, lddw=64), QAMW_EINVAL),
+    (_cex, dict(dX=None), QAMW_ENULL), (_cex, dict(lddx=63), QAMW_EINVAL), (_cex, dict(piece=0), QAMW_EINVAL),
+    (_cex, dict(wb=16), QAMW_EWORKSPACE), (_cex, dict(K=12), QAMW_EINVAL),
+])
+def test_cross_entropy_rejects_bad_arguments(lib, call, kw, rc):
+    assert call(lib, **kw) == rc
+    assert lib.qamw_last_error()

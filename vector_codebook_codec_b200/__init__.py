@@ -79,6 +79,15 @@ _SIGNATURES = {
     "qamw_mx4_unpack_scales": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p]),
     "qamw_mx4_matmul": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_p, ctypes.c_int, _c_i64,
                                        _c_p, _c_p]),
+    "qamw_cross_entropy_workspace_bytes": (_c_sz, [_c_i64, _c_i64]),
+    "qamw_cross_entropy_piece": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64,
+                                                _c_p, _c_i64, _c_p, _c_sz, _c_p, _c_p]),
+    "qamw_cross_entropy_finish": (ctypes.c_int, [_c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_sz, _c_p, _c_p, _c_p, _c_p]),
+    "qamw_cross_entropy_grad_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
+    "qamw_cross_entropy_grad_piece": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_i64,
+                                                     _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i32, _c_p, _c_i64,
+                                                     _c_p, _c_sz, _c_p, _c_p]),
+    "qamw_cross_entropy_grad_finish": (ctypes.c_int, [_c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_sz, _c_p]),
     "qamw_lloyd_workspace_bytes": (_c_sz, [_c_i64, _c_i32]),
     "qamw_lloyd_assign": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_p]),
     "qamw_lloyd_update": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_sz, _c_p]),
@@ -160,6 +169,12 @@ qamw_mx4_decode = _raw("qamw_mx4_decode")
 qamw_mx4_pack_scales = _raw("qamw_mx4_pack_scales")
 qamw_mx4_unpack_scales = _raw("qamw_mx4_unpack_scales")
 qamw_mx4_matmul = _raw("qamw_mx4_matmul")
+qamw_cross_entropy_workspace_bytes = _raw("qamw_cross_entropy_workspace_bytes")
+qamw_cross_entropy_piece = _raw("qamw_cross_entropy_piece")
+qamw_cross_entropy_finish = _raw("qamw_cross_entropy_finish")
+qamw_cross_entropy_grad_workspace_bytes = _raw("qamw_cross_entropy_grad_workspace_bytes")
+qamw_cross_entropy_grad_piece = _raw("qamw_cross_entropy_grad_piece")
+qamw_cross_entropy_grad_finish = _raw("qamw_cross_entropy_grad_finish")
 
 
 # ---------------------------------------------------------------------------
@@ -704,6 +719,153 @@ def mx4_linear(W: Mx4, X, out_dtype=None, status=None, stream=None, out=None):
     with _on(W.codes, stream):
         Xq = mx4_quantize(X, W.block, W.seed, W.col_scale, divide=True, status=status)
         return mx4_matmul(W, Xq, out_dtype, status=status, out=out)
+
+
+# ---------------------------------------------------------------------------
+# cross entropy of a head, by pieces of the vocabulary (qamw_cross_entropy_*)
+# ---------------------------------------------------------------------------
+
+VOCAB_TILE = 256
+_DECODED_BYTES = 64 << 20     # a coded head's piece: its bf16 rows stay in L2 until they are multiplied
+_GRAD_BYTES = 256 << 20       # G of a piece of the backward pass
+
+
+class _Head:
+    """The rows of a head, bf16, a piece at a time: a bf16 tensor, or a coded
+    matrix (:class:`Encoded` with its codebook, or :class:`Mx4`) decoded piece
+    by piece into one buffer."""
+
+    def __init__(self, head, codebook):
+        torch = _torch()
+        self.head, self.codebook, self.buffer = head, codebook, None
+        self.coded = isinstance(head, (Encoded, Mx4))
+        if self.coded:
+            self.V, self.K = head.M, head.K
+            self.anchor = head.packed if isinstance(head, Encoded) else head.codes
+        else:
+            _need_cuda("head", head, torch.bfloat16, 2)
+            self.V, self.K = head.shape
+            self.anchor = head
+            _ld(head)
+        if isinstance(head, Encoded):
+            if codebook is None:
+                raise ValueError("an Encoded head needs its codebook")
+            _need_cuda("codebook", codebook, torch.float32, 2)
+            _same_device(self.anchor, codebook=codebook, row_norm=head.row_norm, sigma=head.sigma,
+                         col_scale=head.col_scale)
+            if head.packed.shape[0] != head.M or not head.packed.is_contiguous():
+                raise ValueError("head.packed must be contiguous with a row per vocabulary entry")
+        elif isinstance(head, Mx4):
+            _need_mx4("head", head)
+
+    def rows(self, v0: int, n: int, status):
+        h = self.head
+        if not self.coded:
+            return h[v0:v0 + n]
+        torch = _torch()
+        if self.buffer is None:
+            self.buffer = torch.empty((n, self.K), dtype=torch.bfloat16, device=self.anchor.device)
+        out = self.buffer[:n]
+        if isinstance(h, Mx4):
+            per = (self.K + 127) // 128 * 512       # scale bytes of a 128-row tile
+            part = Mx4(h.codes[v0:v0 + n], h.scales[v0 // 128 * per:(v0 + n + 127) // 128 * per], n, h.K, h.block,
+                       h.seed, h.col_scale, h.divide)
+            return mx4_decode(part, out=out)
+        part = Encoded(h.packed[v0:v0 + n], h.row_norm[v0:v0 + n], h.col_scale, h.sigma, n, h.K, h.block, h.seed,
+                       h.N, h.bits)
+        return decode(part, self.codebook, out=out, status=status)
+
+
+def _piece_rows(V: int, piece, most: int) -> int:
+    if piece is None:
+        piece = max(2048, most // VOCAB_TILE * VOCAB_TILE)
+    if piece < VOCAB_TILE or piece % VOCAB_TILE:
+        raise ValueError(f"piece must be a positive multiple of {VOCAB_TILE}")
+    return min(piece, V)
+
+
+def _ce_inputs(X, head, targets, codebook, status):
+    torch = _torch()
+    _need_cuda("X", X, torch.bfloat16, 2)
+    _need_cuda("targets", targets, torch.int64, 1)
+    h = _Head(head, codebook)
+    _same_device(X, head=h.anchor, targets=targets)
+    _need_status(X, status)
+    if X.shape[1] != h.K:
+        raise ValueError(f"X has {X.shape[1]} columns and the head {h.K}")
+    if targets.shape[0] != X.shape[0]:
+        raise ValueError("targets must have one entry per row of X")
+    if targets.shape[0] > 1 and targets.stride(0) != 1:
+        raise ValueError("targets must be contiguous")
+    return h, _ld(X)
+
+
+def _need_rows(name, t, T, first):
+    torch = _torch()
+    _need_cuda(name, t, torch.float32, 1)
+    _same_device(first, **{name: t})
+    if t.shape[0] != T or (T > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous float32 [{T}]")
+
+
+def cross_entropy(X, head, targets, codebook=None, ignore_index: int = -100, piece=None, status=None, stream=None):
+    """Cross entropy of every token of X (bf16 CUDA tensor [T, K]) under a
+    head, without keeping the logits: returns (loss, lse), float32 [T] each.
+    ``head`` is a bf16 tensor [V, K], an :class:`Encoded` matrix (with its
+    ``codebook``) or an :class:`Mx4`; coded heads are decoded to bf16 ``piece``
+    rows at a time. ``targets`` is int64 [T]; ``ignore_index`` has loss 0."""
+    torch = _torch()
+    h, ldx = _ce_inputs(X, head, targets, codebook, status)
+    T, lib = X.shape[0], load_library()
+    rows = _piece_rows(h.V, piece, _DECODED_BYTES // (2 * h.K) if h.coded else h.V + VOCAB_TILE)
+    with _on(X, stream):
+        nws = int(lib.qamw_cross_entropy_workspace_bytes(T, h.V))
+        ws = torch.empty(nws, dtype=torch.uint8, device=X.device)
+        loss = torch.empty(T, dtype=torch.float32, device=X.device)
+        lse = torch.empty(T, dtype=torch.float32, device=X.device)
+        for v0 in range(0, h.V, rows):
+            n = min(rows, h.V - v0)
+            W = h.rows(v0, n, status)
+            _check("qamw_cross_entropy_piece", lib.qamw_cross_entropy_piece(
+                _ptr(X), T, h.K, ldx, _ptr(W), n, _ld(W), v0, h.V, _ptr(targets), ignore_index, _ptr(ws), nws,
+                _ptr(status), _stream_ptr()))
+        _check("qamw_cross_entropy_finish", lib.qamw_cross_entropy_finish(
+            T, h.V, _ptr(targets), ignore_index, _ptr(ws), nws, _ptr(loss), _ptr(lse), _ptr(status), _stream_ptr()))
+    return loss, lse
+
+
+def cross_entropy_grad(X, head, targets, lse, grad_loss, codebook=None, ignore_index: int = -100, weight_grad=None,
+                       piece=None, status=None, stream=None):
+    """Gradients of :func:`cross_entropy`: (dX bf16 [T, K], dW bf16 [V, K] or
+    None) for ``lse`` of the forward pass and ``grad_loss`` (float32 [T],
+    dL/dloss of every token). dW is the gradient at the bf16 rows of the head;
+    it is formed for a bf16 head and left out for a coded (frozen) one unless
+    ``weight_grad`` says otherwise. The logits are formed again, ``piece``
+    vocabulary entries at a time."""
+    torch = _torch()
+    h, ldx = _ce_inputs(X, head, targets, codebook, status)
+    T, lib = X.shape[0], load_library()
+    _need_rows("lse", lse, T, X)
+    _need_rows("grad_loss", grad_loss, T, X)
+    rows = _piece_rows(h.V, piece, min(_GRAD_BYTES // (2 * max(T, 1)),
+                                       _DECODED_BYTES // (2 * h.K) if h.coded else h.V + VOCAB_TILE))
+    if weight_grad is None:
+        weight_grad = not h.coded
+    with _on(X, stream):
+        nws = int(lib.qamw_cross_entropy_grad_workspace_bytes(T, h.K, rows))
+        ws = torch.empty(nws, dtype=torch.uint8, device=X.device)
+        dX = torch.empty((T, h.K), dtype=torch.bfloat16, device=X.device)
+        dW = torch.empty((h.V, h.K), dtype=torch.bfloat16, device=X.device) if weight_grad else None
+        for v0 in range(0, h.V, rows):
+            n = min(rows, h.V - v0)
+            W = h.rows(v0, n, status)
+            _check("qamw_cross_entropy_grad_piece", lib.qamw_cross_entropy_grad_piece(
+                _ptr(X), T, h.K, ldx, _ptr(W), n, _ld(W), v0, h.V, _ptr(targets), ignore_index, _ptr(lse),
+                _ptr(grad_loss), rows, int(v0 == 0), _ptr(dW[v0:v0 + n] if weight_grad else None), h.K, _ptr(ws), nws,
+                _ptr(status), _stream_ptr()))
+        _check("qamw_cross_entropy_grad_finish", lib.qamw_cross_entropy_grad_finish(
+            T, h.K, rows, _ptr(dX), h.K, _ptr(ws), nws, _stream_ptr()))
+    return dX, dW
 
 
 def rotate_rows(U, block: int, seed: int, inverse: bool = False, stream=None):

@@ -733,6 +733,119 @@ int qamw_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, 
   return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
 }
 
+// Checks shared by the cross entropy's entry points.
+static int check_ce_sizes(int64_t T, int64_t K, int64_t V, const char *fn) {
+  if (T < 1 || T > (int64_t(1) << 24)) return fail(QAMW_EINVAL, "%s: T must be in [1, 2^24] (got %lld)", fn, (long long)T);
+  if (K < 8 || K % 8) return fail(QAMW_EINVAL, "%s: K must be a positive multiple of 8 (got %lld)", fn, (long long)K);
+  if (V < 1) return fail(QAMW_EINVAL, "%s: the vocabulary must have an entry (got %lld)", fn, (long long)V);
+  if (K > (int64_t(1) << 24) || V > (int64_t(1) << 30)) return fail(QAMW_EUNSUPPORTED, "%s: shape too large", fn);
+  return QAMW_OK;
+}
+
+static int check_ce_piece(const CeArgsIn &a, const char *fn) {
+  int rc;
+  if (!a.X || !a.W || !a.targets) return fail(QAMW_ENULL, "%s: X, W and targets must be non-NULL", fn);
+  if ((rc = check_ce_sizes(a.T, a.K, a.V, fn))) return rc;
+  if (a.n < 1 || a.v0 < 0 || a.v0 % QAMW_VOCAB_TILE || a.n > a.V - a.v0)
+    return fail(QAMW_EINVAL, "%s: the piece must start at a multiple of %d and end within the vocabulary "
+                "(v0=%lld, n=%lld, V=%lld)", fn, QAMW_VOCAB_TILE, (long long)a.v0, (long long)a.n, (long long)a.V);
+  if (a.n % QAMW_VOCAB_TILE && a.v0 + a.n != a.V)
+    return fail(QAMW_EINVAL, "%s: a piece before the last must hold a multiple of %d entries (got %lld)", fn,
+                QAMW_VOCAB_TILE, (long long)a.n);
+  if (a.ldx < a.K || a.ldw < a.K || a.ldx % 8 || a.ldw % 8)
+    return fail(QAMW_EINVAL, "%s: ldx (%lld) and ldw (%lld) must be multiples of 8 and >= K", fn, (long long)a.ldx,
+                (long long)a.ldw);
+  if (reinterpret_cast<uintptr_t>(a.X) % 16 || reinterpret_cast<uintptr_t>(a.W) % 16)
+    return fail(QAMW_EINVAL, "%s: X and W must be 16-byte aligned", fn);
+  if (reinterpret_cast<uintptr_t>(a.targets) % 8) return fail(QAMW_EINVAL, "%s: targets must be 8-byte aligned", fn);
+  return QAMW_OK;
+}
+
+static int check_ce_workspace(const void *workspace, size_t bytes, size_t need, const char *fn) {
+  if (workspace == nullptr || bytes < need)
+    return fail(QAMW_EWORKSPACE, "%s: workspace of %zu bytes needed (got %zu)", fn, need, bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(QAMW_EINVAL, "%s: workspace must be 256-byte aligned", fn);
+  return QAMW_OK;
+}
+
+size_t qamw_cross_entropy_workspace_bytes(int64_t T, int64_t V) {
+  if (T < 1 || T > (int64_t(1) << 24) || V < 1 || V > (int64_t(1) << 30)) return 0;
+  return ce_workspace(T, V).total;
+}
+
+int qamw_cross_entropy_piece(const void *X, int64_t T, int64_t K, int64_t ldx, const void *W, int64_t n, int64_t ldw,
+                             int64_t v0, int64_t V, const int64_t *targets, int64_t ignore_index, void *workspace,
+                             size_t workspace_bytes, int32_t *status, qamw_stream_t stream) {
+  static const char *fn = "qamw_cross_entropy_piece";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  CeArgsIn a{X, T, K, ldx, W, n, ldw, v0, V, targets, ignore_index, status};
+  if ((rc = check_ce_piece(a, fn))) return rc;
+  if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_workspace(T, V).total, fn))) return rc;
+  cudaError_t e = launch_ce_piece(a, workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
+int qamw_cross_entropy_finish(int64_t T, int64_t V, const int64_t *targets, int64_t ignore_index, void *workspace,
+                              size_t workspace_bytes, float *loss, float *lse, int32_t *status, qamw_stream_t stream) {
+  static const char *fn = "qamw_cross_entropy_finish";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  if (!targets || !loss || !lse) return fail(QAMW_ENULL, "%s: targets, loss and lse must be non-NULL", fn);
+  if ((rc = check_ce_sizes(T, 8, V, fn))) return rc;
+  if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_workspace(T, V).total, fn))) return rc;
+  CeArgsIn a{nullptr, T, 8, 8, nullptr, V, 8, 0, V, targets, ignore_index, status};
+  cudaError_t e = launch_ce_finish(a, workspace, loss, lse, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
+size_t qamw_cross_entropy_grad_workspace_bytes(int64_t T, int64_t K, int64_t piece) {
+  if (T < 1 || T > (int64_t(1) << 24) || K < 8 || K % 8 || K > (int64_t(1) << 24) || piece < 1 ||
+      piece > (int64_t(1) << 30))
+    return 0;
+  return ce_grad_workspace(T, K, piece).total;
+}
+
+int qamw_cross_entropy_grad_piece(const void *X, int64_t T, int64_t K, int64_t ldx, const void *W, int64_t n,
+                                  int64_t ldw, int64_t v0, int64_t V, const int64_t *targets, int64_t ignore_index,
+                                  const float *lse, const float *grad_loss, int64_t piece, int32_t first, void *dW,
+                                  int64_t lddw, void *workspace, size_t workspace_bytes, int32_t *status,
+                                  qamw_stream_t stream) {
+  static const char *fn = "qamw_cross_entropy_grad_piece";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  CeArgsIn a{X, T, K, ldx, W, n, ldw, v0, V, targets, ignore_index, status};
+  if (!lse || !grad_loss) return fail(QAMW_ENULL, "%s: lse and grad_loss must be non-NULL", fn);
+  if ((rc = check_ce_piece(a, fn))) return rc;
+  if (piece < n || piece > (int64_t(1) << 30))
+    return fail(QAMW_EINVAL, "%s: piece (%lld) must be at least n (%lld)", fn, (long long)piece, (long long)n);
+  if (dW != nullptr && (lddw < K || reinterpret_cast<uintptr_t>(dW) % 2))
+    return fail(QAMW_EINVAL, "%s: lddw (%lld) must be >= K and dW 2-byte aligned", fn, (long long)lddw);
+  if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_grad_workspace(T, K, piece).total, fn))) return rc;
+  cudaError_t e = launch_ce_grad_piece(a, lse, grad_loss, piece, first != 0, dW, lddw, workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
+int qamw_cross_entropy_grad_finish(int64_t T, int64_t K, int64_t piece, void *dX, int64_t lddx, void *workspace,
+                                   size_t workspace_bytes, qamw_stream_t stream) {
+  static const char *fn = "qamw_cross_entropy_grad_finish";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  if (!dX) return fail(QAMW_ENULL, "%s: dX must be non-NULL", fn);
+  if ((rc = check_ce_sizes(T, K, 1, fn))) return rc;
+  if (piece < 1 || piece > (int64_t(1) << 30)) return fail(QAMW_EINVAL, "%s: piece must be in [1, 2^30]", fn);
+  if (lddx < K || reinterpret_cast<uintptr_t>(dX) % 2)
+    return fail(QAMW_EINVAL, "%s: lddx (%lld) must be >= K and dX 2-byte aligned", fn, (long long)lddx);
+  if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_grad_workspace(T, K, piece).total, fn))) return rc;
+  cudaError_t e = launch_ce_grad_finish(T, K, piece, dX, lddx, workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
 int qamw_selftest_wait_timeout(uint32_t tries, int32_t *status, qamw_stream_t stream) {
   static const char *fn = "qamw_selftest_wait_timeout";
   CallRange nvtx_range(fn);

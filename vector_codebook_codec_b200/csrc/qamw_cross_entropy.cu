@@ -1,0 +1,649 @@
+// qamw_cross_entropy.cu -- softmax cross entropy of a model's head without
+// keeping the logits, and its gradient, a piece of the vocabulary at a time.
+//
+//   l_tv = sum_j X_tj W_vj;  lse_t = log sum_v exp l_tv;  loss_t = lse_t - l_t,target(t)
+//   G_tv = g_t (exp(l_tv - lse_t) - [v = target(t)]);  dX = G W;  dW = G^T X
+//
+// All three products run through one tcgen05 kernel (bf16 operands, fp32
+// accumulation in tensor memory) whose epilogue consumes the accumulators
+// where they are: the forward pass reduces a tile's 256 logits of a token to
+// their maximum and sum of exponentials (8 bytes leave the SM instead of 1024),
+// the backward pass turns them into G. G of one piece is the only matrix of
+// that size that exists, rounded to bf16 once (2^-8 relative at most): bf16 is
+// the operand type that W and X have, and one tcgen05 product takes one type.
+//
+// A tile is 256 rows x 256 columns for a pair of CTAs (cta_group::2, 128
+// accumulator rows each; every CTA loads half of both operands), or 128 x 256
+// for one CTA when there are at most 128 rows.
+#include <algorithm>
+
+#include "qamw_device.cuh"
+#include "qamw_internal.h"
+#include "qamw_tcgen05.cuh"
+
+namespace qamw {
+namespace {
+
+constexpr int kBN = 256;          // columns per tile
+constexpr int kBK = 64;           // contraction per stage: 128 bytes of bf16
+constexpr int kThreads = 192;     // warp 0: loads, warp 1: MMA, warps 2-5: epilogue
+constexpr int kBox = 64 * 128;    // bytes of a 64 x 64 box
+constexpr int kMaxStages = 6;
+constexpr int kGroupRows = 16;    // row tiles walked together (their operand stays in L2)
+
+enum Epilogue { kStats = 0, kGrad = 1, kStore = 2, kSlot = 3 };
+
+struct CeArgs {
+  int64_t rows, cols, depth;      // of the product: D[rows][cols], contraction over depth
+  int64_t n_r, n_c;               // tiles
+  int splits;                     // contraction split (kSlot only)
+  int64_t steps_per_split;
+  int stages;
+  int32_t *status;
+  // kStats, kGrad: rows are tokens, columns the vocabulary entries v0 ..
+  const int64_t *targets;         // [T]
+  int64_t v0, V, ignore;
+  float2 *partials;               // kStats: [tiles of the whole vocabulary][T] (max * log2 e, sum relative to it)
+  float *target_logit;            // kStats: [T]
+  const float *lse, *grad;        // kGrad: [T]
+  __nv_bfloat16 *out;             // kGrad: G, kStore: D
+  int64_t ldo;
+  float *slots;                   // kSlot: [splits][rows][cols] fp32
+  int add;                        // kSlot: add to the slots instead of writing them
+};
+
+template <int CTAS>
+struct CeTile {
+  static constexpr int kRows = 128 * CTAS;                  // rows per tile
+  static constexpr int kColsHere = kBN / CTAS;              // operand columns that one CTA loads
+  static constexpr int kA = 128 * 128;                      // bytes per stage
+  static constexpr int kB = kColsHere * 128;
+  static constexpr int kStage = kA + kB;
+};
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+  return r;
+}
+
+// Operand descriptor, 128-byte swizzle, rows (or columns) of the product
+// contiguous: a 64 x 64 box holds 64 contraction rows of 128 bytes; 8-row atoms
+// are 1024 bytes apart along the contraction, boxes 8192 bytes along the rows.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5, %5, %5, %5, %5}, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u)
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  if constexpr (CTAS == 1)
+    tc::commit(bar);
+  else   // to the barrier of both CTAs
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar,
+                                         uint32_t leader_bar) {
+  if constexpr (CTAS == 1)
+    tc::load_2d(dst, map, x, y, bar);
+  else   // into this CTA's memory, counted at the leader's barrier
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(leader_bar)
+        : "memory");
+}
+
+struct Unit {                     // one tile (and contraction range) of the walk
+  int64_t rt, ct;
+  int split;
+  int64_t k0, k1;                 // contraction steps
+};
+__device__ __forceinline__ Unit unit_of(const CeArgs &g, int64_t u) {
+  Unit r;
+  const int64_t tiles = g.n_r * g.n_c;
+  r.split = (int)(u / tiles);
+  const int64_t t = u - r.split * tiles;
+  // groups of kGroupRows row tiles; inside a group the row varies fastest
+  const int64_t per = kGroupRows * g.n_c, grp = t / per, in = t - grp * per;
+  const int64_t left = g.n_r - grp * kGroupRows, h = left < kGroupRows ? left : kGroupRows;
+  r.ct = in / h;
+  r.rt = grp * kGroupRows + (in - r.ct * h);
+  const int64_t all = (g.depth + kBK - 1) / kBK;
+  r.k0 = r.split * g.steps_per_split;
+  r.k1 = r.k0 + g.steps_per_split < all ? r.k0 + g.steps_per_split : all;
+  if (r.k0 > all) r.k0 = all;
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// A_MN / B_MN: the operand lies [contraction][rows or columns] in memory.
+template <int CTAS, bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+    ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, CeArgs g) {
+  using L = CeTile<CTAS>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int fail_flag;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  volatile int *fail = &fail_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CTAS == 1 ? 0u : cta_rank();
+  const int S = g.stages;
+  uint8_t *sA = smem, *sB = smem + (size_t)S * L::kA;
+
+  if (threadIdx.x == 0) {
+    fail_flag = 0;
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4 * CTAS);
+    }
+    mbar_init(&drained, 1);
+    tc::mbar_init_fence();
+  }
+  if (warp == 1) {
+    if constexpr (CTAS == 1) tc::alloc(&tmem_slot, 512);
+    else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();   // both CTAs' barriers exist before either is signalled
+  tc::fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int64_t n_units = g.n_r * g.n_c * g.splits, step = gridDim.x / CTAS, first = blockIdx.x / CTAS;
+  uint32_t bad = 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t u = first; u < n_units && ok; u += step) {
+        const Unit w = unit_of(g, u);
+        const int r0 = (int)(w.rt * L::kRows + rank * 128), c0 = (int)(w.ct * kBN + rank * L::kColsHere);
+        for (int64_t k = w.k0; k < w.k1; ++k, ++it) {
+          const uint32_t s = it % S;
+          if (!tc::wait(&empty[s], ((it / S) & 1u) ^ 1u, fail)) { ok = false; break; }
+          const uint32_t lb = CTAS == 1 ? 0u : leader_addr(&full[s]);
+          // the leader's barrier counts the bytes of both CTAs
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * L::kStage);
+          uint8_t *a = sA + (size_t)s * L::kA, *b = sB + (size_t)s * L::kB;
+          const int x = (int)(k * kBK);
+          if constexpr (A_MN) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) load_box<CTAS>(a + i * kBox, &amap, r0 + 64 * i, x, &full[s], lb);
+          } else {
+            load_box<CTAS>(a, &amap, x, r0, &full[s], lb);
+          }
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int i = 0; i < L::kColsHere / 64; ++i)
+              load_box<CTAS>(b + i * kBox, &bmap, c0 + 64 * i, x, &full[s], lb);
+          } else {
+#pragma unroll
+            for (int i = 0; i < L::kColsHere / 128; ++i)
+              load_box<CTAS>(b + i * 2 * kBox, &bmap, x, c0 + 128 * i, &full[s], lb);
+          }
+        }
+      }
+      if (*fail) {   // leave no copy in flight behind (the leader's barriers count both CTAs')
+        if (rank == 0) {
+          const uint32_t from = it > (uint32_t)S ? it - S : 0;
+          for (uint32_t i = from; i < it; ++i) mbar_wait(&full[i % S], (i / S) & 1u, tc::kWaitTries);
+        }
+        bad |= QAMW_STATUS_TIMEOUT;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // bf16 x bf16 -> fp32; bits 15, 16: operand rows contiguous
+      constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) |
+                                  ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(kBN >> 3) << 17) |
+                                  ((uint32_t)(L::kRows >> 4) << 24);
+      uint32_t it = 0, seg = 0;
+      bool ok = true;
+      for (int64_t u = first; u < n_units && ok; u += step) {
+        const Unit w = unit_of(g, u);
+        if (w.k0 >= w.k1) continue;
+        const uint32_t buf = seg & 1u;
+        if (!tc::wait(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u, fail)) break;
+        tc::fence_after();
+        const uint32_t d = tmem + buf * kBN;
+        for (int64_t k = w.k0; k < w.k1; ++k, ++it) {
+          const uint32_t s = it % S;
+          if (!tc::wait(&full[s], (it / S) & 1u, fail)) { ok = false; break; }
+          tc::fence_after();
+          const uint32_t a = smem_u32(sA + (size_t)s * L::kA), b = smem_u32(sB + (size_t)s * L::kB);
+#pragma unroll
+          for (int i = 0; i < kBK / 16; ++i)
+            mma_bf16<CTAS>(d, A_MN ? desc_mn_sw128(a + 2048 * i) : tc::desc_k_sw128(a + 32 * i),
+                           B_MN ? desc_mn_sw128(b + 2048 * i) : tc::desc_k_sw128(b + 32 * i), kIdesc,
+                           (k != w.k0 || i != 0) ? 1u : 0u);
+          commit<CTAS>(&empty[s]);
+        }
+        if (ok) commit<CTAS>(&acc_full[buf]);
+        ++seg;
+      }
+      if (*fail) {
+        commit<CTAS>(&drained);
+        mbar_wait(&drained, 0u, tc::kWaitTries);
+        bad |= QAMW_STATUS_TIMEOUT;
+      }
+    }
+  } else {
+    const int wq = warp & 3;
+    uint32_t seg = 0;
+    for (int64_t u = first; u < n_units; u += step) {
+      const Unit w = unit_of(g, u);
+      if (w.k0 >= w.k1) {                  // a split without work: its slot is still a term of the sum
+        if constexpr (EPI == kSlot) {
+          const int64_t r = w.rt * L::kRows + rank * 128 + 32 * wq + lane;
+          if (!g.add && r < g.rows)
+            for (int64_t c = w.ct * kBN; c < g.cols && c < (w.ct + 1) * kBN; ++c)
+              g.slots[((int64_t)w.split * g.rows + r) * g.cols + c] = 0.0f;
+        }
+        continue;
+      }
+      const uint32_t buf = seg & 1u;
+      if (!tc::wait(&acc_full[buf], (seg >> 1) & 1u, fail)) { bad |= QAMW_STATUS_TIMEOUT; break; }
+      __syncwarp();
+      tc::fence_after();
+      const int64_t row = w.rt * L::kRows + rank * 128 + 32 * wq + lane;
+      const int64_t col0 = w.ct * kBN;
+      const int n_cols = (int)(g.cols - col0 < kBN ? g.cols - col0 : kBN);
+      const bool in = row < g.rows;
+      const uint32_t taddr = tmem + buf * kBN + ((uint32_t)(32 * wq) << 16);
+      int tcol = -1;                       // the target's column in this tile
+      float m = -INFINITY, sum = 0.0f;     // kStats
+      float lse2 = 0.0f, gr = 0.0f;        // kGrad
+      if constexpr (EPI == kStats || EPI == kGrad) {
+        const int64_t t = in ? g.targets[row] : g.ignore;
+        const bool live = t != g.ignore && t >= 0 && t < g.V;
+        const int64_t off = t - (g.v0 + col0);
+        if (live && off >= 0 && off < n_cols) tcol = (int)off;
+        if constexpr (EPI == kGrad) {
+          lse2 = in ? g.lse[row] * kLog2e : 0.0f;
+          gr = live ? g.grad[row] : 0.0f;
+        }
+      }
+      for (int c = 0; c < n_cols; c += 32) {
+        float v[32];
+        tc::ld32(taddr + (uint32_t)c, v);
+        const int n = n_cols - c < 32 ? n_cols - c : 32;
+        if constexpr (EPI == kStats) {
+          if (tcol >= c && tcol < c + 32) {
+            float z = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z = (j == tcol - c) ? v[j] : z;
+            g.target_logit[row] = z;
+          }
+          if (n < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = j < n ? v[j] : -INFINITY;
+          }
+          float top = v[0];
+#pragma unroll
+          for (int j = 1; j < 32; ++j) top = fmaxf(top, v[j]);
+          // the reference in units of log 2; a row of -Inf so far has none
+          const float mn = fmaxf(m, top * kLog2e), ref = mn == -INFINITY ? 0.0f : mn;
+          sum *= exp2f(m - ref);
+          m = mn;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum += exp2f(__fmaf_rn(v[j], kLog2e, -ref));
+        } else if constexpr (EPI == kGrad) {
+          const bool none = gr == 0.0f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float p = exp2f(__fmaf_rn(v[j], kLog2e, -lse2));
+            if (j == tcol - c) p -= 1.0f;
+            v[j] = none ? 0.0f : gr * p;
+          }
+        }
+        if constexpr (EPI == kGrad || EPI == kStore) {
+          if (in) {
+            __nv_bfloat16 *o = g.out + row * g.ldo + col0 + c;
+            if (n == 32 && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                __nv_bfloat162 h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+                reinterpret_cast<uint4 *>(o)[i] = *reinterpret_cast<const uint4 *>(h);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j < n) o[j] = __float2bfloat16_rn(v[j]);
+            }
+          }
+        }
+        if constexpr (EPI == kSlot) {
+          if (in) {   // cols % 8 == 0: 16-byte groups are all in or all out
+            float4 *o = reinterpret_cast<float4 *>(g.slots + ((int64_t)w.split * g.rows + row) * g.cols + col0 + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (4 * i < n) {
+                float4 q = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                if (g.add) {
+                  const float4 p = o[i];
+                  q.x += p.x, q.y += p.y, q.z += p.z, q.w += p.w;
+                }
+                o[i] = q;
+              }
+            }
+          }
+        }
+      }
+      if constexpr (EPI == kStats)
+        if (in) g.partials[((g.v0 + col0) / kBN) * g.rows + row] = make_float2(m, sum);
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CTAS == 1) tc::mbar_arrive(&acc_empty[buf]);
+        else
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(&acc_empty[buf]))
+                       : "memory");
+      }
+      ++seg;
+    }
+  }
+
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();   // no CTA leaves while the pair's MMAs, copies or arrivals may reach it
+  if (warp == 1) {
+    tc::fence_after();
+    if constexpr (CTAS == 1) tc::dealloc(tmem, 512);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (lane == 0) status_or(g.status, bad);
+}
+
+// loss and normaliser from the tiles' partial maxima and sums: 8 threads per
+// token take every eighth tile, then join in a fixed order.
+__global__ void __launch_bounds__(256) ce_finish_kernel(const float2 *partials, const float *target_logit,
+                                                        const int64_t *targets, int64_t T, int64_t V, int64_t n_tiles,
+                                                        int64_t ignore, float *loss, float *lse, int32_t *status) {
+  __shared__ float2 part[8][32];
+  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.0f;
+  auto join = [&](float2 p) {
+    const float mn = fmaxf(m, p.x), ref = mn == -INFINITY ? 0.0f : mn;
+    s = s * exp2f(m - ref) + p.y * exp2f(p.x - ref);
+    m = mn;
+  };
+  if (t < T)
+    for (int64_t i = sl; i < n_tiles; i += 8) join(partials[i * T + t]);
+  part[sl][lane] = make_float2(m, s);
+  __syncthreads();
+  if (sl != 0 || t >= T) return;
+  for (int i = 1; i < 8; ++i) join(part[i][lane]);
+  const float n = __fmaf_rn(m, kLn2, logf(s));
+  const int64_t at = targets[t];
+  const bool real = at >= 0 && at < V;
+  if (at != ignore && !real) status_or(status, QAMW_STATUS_BAD_INDEX);
+  lse[t] = n;
+  loss[t] = (at != ignore && real) ? n - target_logit[t] : 0.0f;
+}
+
+// X with the rows of ignored tokens set to zero, [T][K]: their G is zero, but
+// dW = G^T X would still turn an Inf or NaN of a padded row into NaN. Eight
+// columns a thread.
+__global__ void __launch_bounds__(256) ce_live_rows_kernel(const uint4 *X, int64_t ldx8, const int64_t *targets,
+                                                           int64_t T, int64_t K8, int64_t V, int64_t ignore,
+                                                           uint4 *out) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * K8; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / K8, c = i - t * K8, at = targets[t];
+    out[i] = (at != ignore && at >= 0 && at < V) ? X[t * ldx8 + c] : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// dX = the sum of the slots, in order, rounded to bf16 (four values a thread)
+__global__ void __launch_bounds__(256) ce_sum_slots_kernel(const float *slots, int splits, int64_t T, int64_t K,
+                                                           __nv_bfloat16 *dX, int64_t ldx) {
+  const int64_t n = T * K / 4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float4 a = reinterpret_cast<const float4 *>(slots)[i];
+    for (int s = 1; s < splits; ++s) {
+      const float4 b = reinterpret_cast<const float4 *>(slots + (int64_t)s * T * K)[i];
+      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    const int64_t row = 4 * i / K, col = 4 * i % K;
+    __nv_bfloat16 *o = dX + row * ldx + col;
+    o[0] = __float2bfloat16_rn(a.x);
+    o[1] = __float2bfloat16_rn(a.y);
+    o[2] = __float2bfloat16_rn(a.z);
+    o[3] = __float2bfloat16_rn(a.w);
+  }
+}
+
+// [rows][cols] bf16 in memory, boxes of box_c x box_r
+bool make_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t ld, int box_r, int box_c) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {(cuuint32_t)box_c, (cuuint32_t)box_r};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operand {
+  const void *p;
+  int64_t rows, cols, ld;         // as it lies in memory
+};
+
+template <int CTAS, bool A_MN, bool B_MN, int EPI>
+cudaError_t run(const Operand &A, const Operand &B, CeArgs g, cudaStream_t s) {
+  using L = CeTile<CTAS>;
+  CUtensorMap amap, bmap;
+  if (!make_map(&amap, A.p, A.rows, A.cols, A.ld, A_MN ? 64 : 128, 64) ||
+      !make_map(&bmap, B.p, B.rows, B.cols, B.ld, B_MN ? 64 : 128, 64))
+    return cudaErrorInvalidValue;
+  int dev = 0, smem_max = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+  g.n_r = (g.rows + L::kRows - 1) / L::kRows;
+  g.n_c = (g.cols + kBN - 1) / kBN;
+  g.stages = (int)std::min<int64_t>(kMaxStages, (smem_max - 2048) / L::kStage);
+  const size_t smem = 1024 + (size_t)g.stages * L::kStage;
+  auto kern = ce_gemm_kernel<CTAS, A_MN, B_MN, EPI>;
+  if ((e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(CTAS * std::min<int64_t>(sm_count() / CTAS, g.n_r * g.n_c * g.splits)), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, amap, bmap, g);
+}
+
+// one CTA per tile when 128 rows hold everything, else a pair
+template <bool A_MN, bool B_MN, int EPI>
+cudaError_t run_rows(const Operand &A, const Operand &B, const CeArgs &g, cudaStream_t s) {
+  return g.rows <= 128 ? run<1, A_MN, B_MN, EPI>(A, B, g, s) : run<2, A_MN, B_MN, EPI>(A, B, g, s);
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+int64_t vocab_tiles(int64_t V) { return (V + kBN - 1) / kBN; }
+
+// Contraction splits of dX for pieces of `piece` vocabulary entries: the
+// smallest number that fills the machine's waves to 90% (or the fullest up to
+// 32), each split at least 8 steps long.
+int dx_splits(int64_t T, int64_t K, int64_t piece) {
+  const int ctas = T <= 128 ? 1 : 2;
+  const int64_t tiles = ((T + 128 * ctas - 1) / (128 * ctas)) * ((K + kBN - 1) / kBN);
+  const int64_t slots = sm_count() / ctas, steps = (piece + kBK - 1) / kBK;
+  int best = 1;
+  double best_fill = 0.0;
+  for (int s = 1; s <= 32 && (s == 1 || steps / s >= 8); ++s) {
+    const int64_t units = tiles * s, waves = (units + slots - 1) / slots;
+    const double fill = (double)units / (double)(waves * slots);
+    if (fill > best_fill) best = s, best_fill = fill;
+    if (fill >= 0.9) break;
+  }
+  return best;
+}
+
+}  // namespace
+
+CeWorkspace ce_workspace(int64_t T, int64_t V) {
+  CeWorkspace w;
+  w.target_logit = align256((size_t)vocab_tiles(V) * (size_t)T * sizeof(float2));
+  w.total = w.target_logit + align256((size_t)T * 4);
+  return w;
+}
+
+CeGradWorkspace ce_grad_workspace(int64_t T, int64_t K, int64_t piece) {
+  CeGradWorkspace w;
+  w.ldg = (piece + 7) / 8 * 8;
+  w.live = align256((size_t)T * (size_t)w.ldg * 2);
+  w.slots = w.live + align256((size_t)T * (size_t)K * 2);
+  w.splits = dx_splits(T, K, piece);
+  w.total = w.slots + align256((size_t)w.splits * (size_t)T * (size_t)K * 4);
+  return w;
+}
+
+cudaError_t launch_ce_piece(const CeArgsIn &a, void *workspace, cudaStream_t s) {
+  const CeWorkspace w = ce_workspace(a.T, a.V);
+  CeArgs g = {};
+  g.rows = a.T;
+  g.cols = a.n;
+  g.depth = a.K;
+  g.splits = 1;
+  g.steps_per_split = (a.K + kBK - 1) / kBK;
+  g.status = a.status;
+  g.targets = a.targets;
+  g.v0 = a.v0;
+  g.V = a.V;
+  g.ignore = a.ignore;
+  g.partials = static_cast<float2 *>(workspace);
+  g.target_logit = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + w.target_logit);
+  return run_rows<false, false, kStats>({a.X, a.T, a.K, a.ldx}, {a.W, a.n, a.K, a.ldw}, g, s);
+}
+
+cudaError_t launch_ce_finish(const CeArgsIn &a, void *workspace, float *loss, float *lse, cudaStream_t s) {
+  const CeWorkspace w = ce_workspace(a.T, a.V);
+  ce_finish_kernel<<<(unsigned)((a.T + 31) / 32), 256, 0, s>>>(
+      static_cast<const float2 *>(workspace),
+      reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.target_logit), a.targets, a.T, a.V,
+      vocab_tiles(a.V), a.ignore, loss, lse, a.status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const float *grad, int64_t piece, bool first,
+                                 void *dW, int64_t lddw, void *workspace, cudaStream_t s) {
+  const CeGradWorkspace w = ce_grad_workspace(a.T, a.K, piece);
+  __nv_bfloat16 *G = static_cast<__nv_bfloat16 *>(workspace);
+  uint4 *live = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(workspace) + w.live);
+  if (first) {
+    const int64_t blocks = (a.T * a.K / 8 + 255) / 256, most = (int64_t)sm_count() * 16;
+    ce_live_rows_kernel<<<(unsigned)std::min(blocks, most), 256, 0, s>>>(
+        static_cast<const uint4 *>(a.X), a.ldx / 8, a.targets, a.T, a.K / 8, a.V, a.ignore, live);
+    const cudaError_t c = cudaGetLastError();
+    if (c != cudaSuccess) return c;
+  }
+  const Operand X{live, a.T, a.K, a.K};
+  CeArgs g = {};
+  g.rows = a.T;
+  g.cols = a.n;
+  g.depth = a.K;
+  g.splits = 1;
+  g.steps_per_split = (a.K + kBK - 1) / kBK;
+  g.status = a.status;
+  g.targets = a.targets;
+  g.v0 = a.v0;
+  g.V = a.V;
+  g.ignore = a.ignore;
+  g.lse = lse;
+  g.grad = grad;
+  g.out = G;
+  g.ldo = w.ldg;
+  cudaError_t e = run_rows<false, false, kGrad>(X, {a.W, a.n, a.K, a.ldw}, g, s);
+  if (e != cudaSuccess) return e;
+  CeArgs x = {};
+  x.rows = a.T;
+  x.cols = a.K;
+  x.depth = a.n;
+  x.splits = w.splits;
+  x.steps_per_split = ((a.n + kBK - 1) / kBK + w.splits - 1) / w.splits;
+  x.status = a.status;
+  x.slots = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + w.slots);
+  x.add = first ? 0 : 1;
+  if ((e = run_rows<false, true, kSlot>({G, a.T, a.n, w.ldg}, {a.W, a.n, a.K, a.ldw}, x, s)) != cudaSuccess) return e;
+  if (dW == nullptr) return cudaSuccess;
+  CeArgs d = {};
+  d.rows = a.n;
+  d.cols = a.K;
+  d.depth = a.T;
+  d.splits = 1;
+  d.steps_per_split = (a.T + kBK - 1) / kBK;
+  d.status = a.status;
+  d.out = static_cast<__nv_bfloat16 *>(dW);
+  d.ldo = lddw;
+  return run_rows<true, true, kStore>({G, a.T, a.n, w.ldg}, X, d, s);
+}
+
+cudaError_t launch_ce_grad_finish(int64_t T, int64_t K, int64_t piece, void *dX, int64_t lddx, void *workspace,
+                                  cudaStream_t s) {
+  const CeGradWorkspace w = ce_grad_workspace(T, K, piece);
+  const int64_t blocks = (T * K / 4 + 255) / 256, most = (int64_t)sm_count() * 16;
+  ce_sum_slots_kernel<<<(unsigned)std::min(blocks, most), 256, 0, s>>>(
+      reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.slots), w.splits, T, K,
+      static_cast<__nv_bfloat16 *>(dX), lddx);
+  return cudaGetLastError();
+}
+
+}  // namespace qamw

@@ -218,6 +218,35 @@ struct Mx4MatmulArgs {
 };
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs &a, cudaStream_t s);
 
+// Cross entropy of a head and its gradient by pieces of the vocabulary
+// (qamw_cross_entropy.cu): X bf16 [T][ldx], a piece of W bf16 [n][ldw] that
+// holds the vocabulary entries v0 .. v0 + n - 1 of V; v0 % 256 == 0, K % 8 == 0.
+struct CeArgsIn {
+  const void *X;
+  int64_t T, K, ldx;
+  const void *W;
+  int64_t n, ldw, v0, V;
+  const int64_t *targets;  // [T]
+  int64_t ignore;
+  int32_t *status;
+};
+struct CeWorkspace {       // tile maxima and sums, then the targets' logits [T]
+  size_t target_logit, total;
+};
+CeWorkspace ce_workspace(int64_t T, int64_t V);
+cudaError_t launch_ce_piece(const CeArgsIn &a, void *workspace, cudaStream_t s);
+cudaError_t launch_ce_finish(const CeArgsIn &a, void *workspace, float *loss, float *lse, cudaStream_t s);
+struct CeGradWorkspace {   // G bf16 [T][ldg], X without its ignored rows bf16 [T][K], the fp32 slots of dX [splits][T][K]
+  int64_t ldg;
+  size_t live, slots, total;
+  int splits;
+};
+CeGradWorkspace ce_grad_workspace(int64_t T, int64_t K, int64_t piece);
+cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const float *grad, int64_t piece, bool first,
+                                 void *dW, int64_t lddw, void *workspace, cudaStream_t s);
+cudaError_t launch_ce_grad_finish(int64_t T, int64_t K, int64_t piece, void *dX, int64_t lddx, void *workspace,
+                                  cudaStream_t s);
+
 // Lloyd training of the 2D codebook (qamw_lloyd.cu); points and centroids are
 // fp64 [.][2], 16-byte aligned.
 size_t lloyd_workspace_bytes(int64_t T, int N);
