@@ -438,6 +438,22 @@ int qamw_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, 
                     int32_t *status, qamw_stream_t stream);
 
 /*
+ * qamw_mx4_linear -- qamw_mx4_quantize of the activations X (device [T][ldx] of
+ * x_dtype; divided by col_scale, rotated with block and sign_seed, all as the
+ * weights were quantised) into the workspace, then qamw_mx4_matmul with the
+ * coded weights: a layer's product in one call. Y equals that of the two calls
+ * bit for bit. workspace: device, 256-byte aligned,
+ * qamw_mx4_linear_workspace_bytes(T, K) = align256(T K / 2) +
+ * qamw_mx4_scale_bytes(T, K) bytes (0 if the shape is invalid).
+ * Errors: as the two calls, plus QAMW_EWORKSPACE.
+ */
+int qamw_mx4_linear(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, const void *X, qamw_dtype x_dtype,
+                    int64_t T, int64_t K, int64_t ldx, const float *col_scale, int32_t block, uint64_t sign_seed,
+                    void *Y, qamw_dtype out_dtype, int64_t ldy, void *workspace, size_t workspace_bytes,
+                    int32_t *status, qamw_stream_t stream);
+size_t qamw_mx4_linear_workspace_bytes(int64_t T, int64_t K);
+
+/*
  * Softmax cross entropy of a model's head, without keeping the logits, and its
  * gradient -- the quantity by which the pages judge a coded model (its
  * perplexity is exp of the mean loss).

@@ -292,6 +292,13 @@ def _mxm(lib, **kw):
     return lib.qamw_mx4_matmul(*a.values(), None, None)
 
 
+def _mxl(lib, **kw):
+    a = dict(wc=FAKE, ws=FAKE, M=8, X=FAKE, xt=1, T=4, K=256, ldx=256, s=None, block=128, seed=1, Y=FAKE, ot=0, ldy=8,
+             work=FAKE, wb=1 << 40)
+    a.update(kw)
+    return lib.qamw_mx4_linear(*a.values(), None, None)
+
+
 ODD = ctypes.c_void_p(0x10001)
 
 
@@ -308,10 +315,22 @@ ODD = ctypes.c_void_p(0x10001)
     (_mxm, dict(wc=None), QAMW_ENULL), (_mxm, dict(xs=None), QAMW_ENULL), (_mxm, dict(Y=None), QAMW_ENULL),
     (_mxm, dict(T=0), QAMW_EINVAL), (_mxm, dict(ldy=7), QAMW_EINVAL), (_mxm, dict(ot=2), QAMW_EINVAL),
     (_mxm, dict(K=100), QAMW_EINVAL), (_mxm, dict(xc=ODD), QAMW_EINVAL),
+    (_mxl, dict(X=None), QAMW_ENULL), (_mxl, dict(Y=None), QAMW_ENULL), (_mxl, dict(wc=None), QAMW_ENULL),
+    (_mxl, dict(T=0), QAMW_EINVAL), (_mxl, dict(ldx=255), QAMW_EINVAL), (_mxl, dict(ldy=7), QAMW_EINVAL),
+    (_mxl, dict(block=6), QAMW_EINVAL), (_mxl, dict(xt=5), QAMW_EINVAL), (_mxl, dict(X=ODD), QAMW_EINVAL),
+    (_mxl, dict(work=None), QAMW_EWORKSPACE), (_mxl, dict(wb=64), QAMW_EWORKSPACE), (_mxl, dict(work=ODD), QAMW_EINVAL),
 ])
 def test_mx4_rejects_bad_arguments(lib, call, kw, rc):
     assert call(lib, **kw) == rc
     assert lib.qamw_last_error()
+
+
+def test_mx4_linear_workspace_bytes(lib):
+    from vector_codebook_codec_b200 import mx4_scale_bytes
+    for T, K in ((1, 32), (37, 5120), (300, 4096)):
+        assert lib.qamw_mx4_linear_workspace_bytes(T, K) == (T * K // 2 + 255) // 256 * 256 + mx4_scale_bytes(T, K)
+        assert mx4_scale_bytes(T, K) == lib.qamw_mx4_scale_bytes(T, K)
+    assert lib.qamw_mx4_linear_workspace_bytes(3, 40) == 0
 
 
 def test_mx4_scale_layout_rejects_bad_arguments(lib):

@@ -77,6 +77,9 @@ _SIGNATURES = {
                                        _c_i64, _c_p]),
     "qamw_mx4_pack_scales": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p]),
     "qamw_mx4_unpack_scales": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p]),
+    "qamw_mx4_linear": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_i32,
+                                       _c_u64, _c_p, ctypes.c_int, _c_i64, _c_p, _c_sz, _c_p, _c_p]),
+    "qamw_mx4_linear_workspace_bytes": (_c_sz, [_c_i64, _c_i64]),
     "qamw_mx4_matmul": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_p, ctypes.c_int, _c_i64,
                                        _c_p, _c_p]),
     "qamw_cross_entropy_workspace_bytes": (_c_sz, [_c_i64, _c_i64]),
@@ -169,6 +172,8 @@ qamw_mx4_decode = _raw("qamw_mx4_decode")
 qamw_mx4_pack_scales = _raw("qamw_mx4_pack_scales")
 qamw_mx4_unpack_scales = _raw("qamw_mx4_unpack_scales")
 qamw_mx4_matmul = _raw("qamw_mx4_matmul")
+qamw_mx4_linear = _raw("qamw_mx4_linear")
+qamw_mx4_linear_workspace_bytes = _raw("qamw_mx4_linear_workspace_bytes")
 qamw_cross_entropy_workspace_bytes = _raw("qamw_cross_entropy_workspace_bytes")
 qamw_cross_entropy_piece = _raw("qamw_cross_entropy_piece")
 qamw_cross_entropy_finish = _raw("qamw_cross_entropy_finish")
@@ -523,12 +528,13 @@ class Mx4:
     divide: bool        # the rows were divided by s (activations) instead of multiplied (weights)
 
 
+_NULL_CONTEXT = contextlib.nullcontext()
+
+
 @contextlib.contextmanager
-def _on(first, stream):
-    """The device of ``first``, and ``stream`` as its current stream, so that
-    what a call allocates for itself belongs to the stream that uses it."""
+def _switched(device, stream):
     torch = _torch()
-    with torch.cuda.device(first.device):
+    with torch.cuda.device(device):
         if stream is None:
             yield
         else:
@@ -536,50 +542,80 @@ def _on(first, stream):
                 yield
 
 
-def _same_device(first, **tensors):
-    """Every tensor given lies on the device of `first`."""
+def _on(device, stream):
+    """``device`` as the current one and ``stream`` as its current stream, so
+    that what a call allocates for itself belongs to the stream that uses it."""
+    if stream is None and device.index == _torch()._C._cuda_getDevice():
+        return _NULL_CONTEXT
+    return _switched(device, stream)
+
+
+def _raw_stream(device):
+    """The current stream of ``device`` as the C ABI takes it."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(device, **tensors):
+    """Every tensor given lies on ``device``."""
     for name, t in tensors.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-def _need_out(name, out, shape, dtype):
-    """A caller's output: right shape and type, unit column stride, rows apart."""
+def _need_out(name, out, shape, dtype, device):
+    """A caller's output: right place, shape and type, unit column stride, rows apart."""
+    _need_cuda(name, out, dtype, len(shape))
+    _same_device(device, **{name: out})
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
-    if out.dtype != dtype:
-        raise ValueError(f"{name} must have dtype {dtype}, got {out.dtype}")
-    if out.dim() == 2 and out.shape[0] > 1 and out.stride(0) < out.shape[1]:
+    if out.shape[0] > 1 and out.stride(0) < out.shape[1]:
         raise ValueError(f"{name} must not have overlapping rows")
+    return _ld(out)
 
 
-def _need_status(first, status):
-    torch = _torch()
-    _need_cuda("status", status, torch.int32)
-    _same_device(first, status=status)
-    if status is not None and status.numel() < 1:
-        raise ValueError("status must hold one int32")
+def _need_status(device, status):
+    if status is not None:
+        _need_cuda("status", status, _torch().int32)
+        _same_device(device, status=status)
+        if status.numel() < 1:
+            raise ValueError("status must hold one int32")
 
 
-def _need_scale(first, col_scale, K):
-    torch = _torch()
-    _need_cuda("col_scale", col_scale, torch.float32, 1)
-    _same_device(first, col_scale=col_scale)
-    if col_scale is not None and (col_scale.shape[0] != K or (K > 1 and col_scale.stride(0) != 1)):
-        raise ValueError("col_scale must be K contiguous values")
+def _need_scale(device, col_scale, K):
+    if col_scale is not None:
+        _need_cuda("col_scale", col_scale, _torch().float32, 1)
+        _same_device(device, col_scale=col_scale)
+        if col_scale.shape[0] != K or (K > 1 and col_scale.stride(0) != 1):
+            raise ValueError("col_scale must be K contiguous values")
+
+
+def mx4_scale_bytes(M: int, K: int) -> int:
+    if M < 1 or K < 32 or K % 32:
+        raise ValueError(f"no microscaled form of a {M} x {K} matrix (K must be a positive multiple of 32)")
+    return (M + 127) // 128 * ((K + 127) // 128) * 512
 
 
 def _need_mx4(name, q):
     """The tensors of an Mx4 agree with its shape (the kernels trust them)."""
     torch = _torch()
-    _need_cuda(f"{name}.codes", q.codes, torch.uint8, 2)
-    _need_cuda(f"{name}.scales", q.scales, torch.uint8, 1)
-    _same_device(q.codes, **{f"{name}.scales": q.scales})
-    if tuple(q.codes.shape) != (q.M, q.K // 2) or not q.codes.is_contiguous():
+    if not isinstance(q, Mx4):
+        raise ValueError(f"{name} must be an Mx4")
+    codes, scales = q.codes, q.scales
+    _need_cuda(f"{name}.codes", codes, torch.uint8, 2)
+    _need_cuda(f"{name}.scales", scales, torch.uint8, 1)
+    if codes.shape != (q.M, q.K // 2) or not codes.is_contiguous():
         raise ValueError(f"{name}.codes must be contiguous [M, K/2]")
-    if q.scales.numel() != mx4_scale_bytes(q.M, q.K) or not q.scales.is_contiguous():
+    if scales.numel() != mx4_scale_bytes(q.M, q.K) or not scales.is_contiguous():
         raise ValueError(f"{name}.scales must be qamw_mx4_scale_bytes(M, K) contiguous bytes")
-    _need_scale(q.codes, q.col_scale, q.K)
+    device = codes.device
+    if scales.device != device:
+        raise ValueError(f"{name}.scales must be on {device}, got {scales.device}")
+    _need_scale(device, q.col_scale, q.K)
+    return device
 
 
 def _out_type(out_dtype):
@@ -591,13 +627,6 @@ def _out_type(out_dtype):
     raise ValueError("out_dtype must be bfloat16 or float32")
 
 
-def mx4_scale_bytes(M: int, K: int) -> int:
-    n = int(load_library().qamw_mx4_scale_bytes(M, K))
-    if n == 0:
-        raise ValueError(f"no microscaled form of a {M} x {K} matrix (K must be a multiple of 32)")
-    return n
-
-
 def mx4_quantize(W, block: int = 0, seed: int = 0, col_scale=None, divide: bool = False, status=None, stream=None,
                  out=None) -> Mx4:
     """W (bf16 or fp32 CUDA tensor [M, K], unit column stride) in microscaled
@@ -607,23 +636,24 @@ def mx4_quantize(W, block: int = 0, seed: int = 0, col_scale=None, divide: bool 
     32 columns. ``out`` = (codes, scales) preallocated, or None."""
     torch = _torch()
     _need_cuda("W", W, ndim=2)
-    wt, ld = _wdtype(W), _ld(W)
+    wt, ld, device = _wdtype(W), _ld(W), W.device
     M, K = W.shape
     n_scales = mx4_scale_bytes(M, K)
-    _need_scale(W, col_scale, K)
-    _need_status(W, status)
-    with _on(W, stream):
+    _need_scale(device, col_scale, K)
+    _need_status(device, status)
+    with _on(device, stream):
         if out is None:
-            codes = torch.empty((M, K // 2), dtype=torch.uint8, device=W.device)
-            scales = torch.empty(n_scales, dtype=torch.uint8, device=W.device)
+            codes = torch.empty((M, K // 2), dtype=torch.uint8, device=device)
+            scales = torch.empty(n_scales, dtype=torch.uint8, device=device)
+            q = Mx4(codes, scales, M, K, block, seed, col_scale, bool(divide))
         else:
             codes, scales = out
-        q = Mx4(codes, scales, M, K, block, seed, col_scale, bool(divide))
-        _need_mx4("out", q)
-        _same_device(W, out=codes)
+            q = Mx4(codes, scales, M, K, block, seed, col_scale, bool(divide))
+            if _need_mx4("out", q) != device:
+                raise ValueError(f"out must be on {device}")
         _check("qamw_mx4_quantize", load_library().qamw_mx4_quantize(
-            _ptr(W), wt, M, K, ld, _ptr(col_scale), int(q.divide), block, seed & (2**64 - 1), _ptr(codes),
-            _ptr(scales), _ptr(status), _stream_ptr(stream)))
+            W.data_ptr(), wt, M, K, ld, _address(col_scale), int(q.divide), block, seed & (2**64 - 1),
+            codes.data_ptr(), scales.data_ptr(), _address(status), _raw_stream(device)))
     return q
 
 
@@ -634,16 +664,16 @@ def mx4_decode(q: Mx4, out_dtype=None, original: bool = True, stream=None, out=N
     torch = _torch()
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     ot = _out_type(out_dtype)
-    _need_mx4("q", q)
-    with _on(q.codes, stream):
+    device = _need_mx4("q", q)
+    with _on(device, stream):
         if out is None:
-            out = torch.empty((q.M, q.K), dtype=out_dtype, device=q.codes.device)
-        _need_cuda("out", out, ndim=2)
-        _need_out("out", out, (q.M, q.K), out_dtype)
-        _same_device(q.codes, out=out)
+            out, ld = torch.empty((q.M, q.K), dtype=out_dtype, device=device), q.K
+        else:
+            ld = _need_out("out", out, (q.M, q.K), out_dtype, device)
         _check("qamw_mx4_decode", load_library().qamw_mx4_decode(
-            _ptr(q.codes), _ptr(q.scales), q.M, q.K, _ptr(q.col_scale) if original else None, int(q.divide),
-            q.block if original else 0, q.seed & (2**64 - 1), _ptr(out), ot, _ld(out), _stream_ptr(stream)))
+            q.codes.data_ptr(), q.scales.data_ptr(), q.M, q.K, _address(q.col_scale) if original else None,
+            int(q.divide), q.block if original else 0, q.seed & (2**64 - 1), out.data_ptr(), ot, ld,
+            _raw_stream(device)))
     return out
 
 
@@ -655,28 +685,30 @@ def mx4_from_parts(codes, scale_rows, block: int = 0, seed: int = 0, col_scale=N
     torch = _torch()
     _need_cuda("codes", codes, torch.uint8, 2)
     _need_cuda("scale_rows", scale_rows, torch.uint8, 2)
-    _same_device(codes, scale_rows=scale_rows)
+    device = codes.device
+    _same_device(device, scale_rows=scale_rows)
     M, K = codes.shape[0], 2 * codes.shape[1]
+    n_scales = mx4_scale_bytes(M, K)
     if tuple(scale_rows.shape) != (M, K // 32):
         raise ValueError(f"scale_rows must be [{M}, {K // 32}]")
-    with _on(codes, stream):
+    with _on(device, stream):
         codes, scale_rows = codes.contiguous(), scale_rows.contiguous()
-        scales = torch.empty(mx4_scale_bytes(M, K), dtype=torch.uint8, device=codes.device)
+        scales = torch.empty(n_scales, dtype=torch.uint8, device=device)
+        q = Mx4(codes, scales, M, K, block, seed, col_scale, bool(divide))
+        _need_mx4("q", q)
         _check("qamw_mx4_pack_scales", load_library().qamw_mx4_pack_scales(
-            _ptr(scale_rows), M, K, _ptr(scales), _stream_ptr(stream)))
-    q = Mx4(codes, scales, M, K, block, seed, col_scale, bool(divide))
-    _need_mx4("q", q)
+            scale_rows.data_ptr(), M, K, scales.data_ptr(), _raw_stream(device)))
     return q
 
 
 def mx4_scale_rows(q: Mx4, stream=None):
     """The e8m0 scale bytes of ``q``, row-major (uint8 [M, K/32])."""
     torch = _torch()
-    _need_mx4("q", q)
-    with _on(q.codes, stream):
-        rows = torch.empty((q.M, q.K // 32), dtype=torch.uint8, device=q.codes.device)
+    device = _need_mx4("q", q)
+    with _on(device, stream):
+        rows = torch.empty((q.M, q.K // 32), dtype=torch.uint8, device=device)
         _check("qamw_mx4_unpack_scales", load_library().qamw_mx4_unpack_scales(
-            _ptr(q.scales), q.M, q.K, _ptr(rows), _stream_ptr(stream)))
+            q.scales.data_ptr(), q.M, q.K, rows.data_ptr(), _raw_stream(device)))
     return rows
 
 
@@ -687,38 +719,56 @@ def mx4_matmul(W: Mx4, X: Mx4, out_dtype=None, status=None, stream=None, out=Non
     torch = _torch()
     out_dtype = torch.float32 if out_dtype is None else out_dtype
     ot = _out_type(out_dtype)
-    _need_mx4("W", W)
-    _need_mx4("X", X)
-    _same_device(W.codes, X=X.codes)
-    _need_status(W.codes, status)
+    device = _need_mx4("W", W)
+    if _need_mx4("X", X) != device:
+        raise ValueError(f"X must be on {device}, got {X.codes.device}")
+    _need_status(device, status)
     if W.K != X.K:
         raise ValueError(f"W has {W.K} columns and X {X.K}")
     if (W.block, W.seed & (2**64 - 1) if W.block else 0) != (X.block, X.seed & (2**64 - 1) if X.block else 0):
         raise ValueError("W and X must be rotated with the same block and seed")
-    with _on(W.codes, stream):
+    with _on(device, stream):
         if out is None:
-            out = torch.empty((X.M, W.M), dtype=out_dtype, device=W.codes.device)
-        _need_cuda("out", out, ndim=2)
-        _need_out("out", out, (X.M, W.M), out_dtype)
-        _same_device(W.codes, out=out)
+            out, ld = torch.empty((X.M, W.M), dtype=out_dtype, device=device), W.M
+        else:
+            ld = _need_out("out", out, (X.M, W.M), out_dtype, device)
         _check("qamw_mx4_matmul", load_library().qamw_mx4_matmul(
-            _ptr(W.codes), _ptr(W.scales), W.M, _ptr(X.codes), _ptr(X.scales), X.M, W.K, _ptr(out), ot, _ld(out),
-            _ptr(status), _stream_ptr(stream)))
+            W.codes.data_ptr(), W.scales.data_ptr(), W.M, X.codes.data_ptr(), X.scales.data_ptr(), X.M, W.K,
+            out.data_ptr(), ot, ld, _address(status), _raw_stream(device)))
     return out
 
 
 def mx4_linear(W: Mx4, X, out_dtype=None, status=None, stream=None, out=None):
     """Y [T, M] = X W^T for a microscaled weight matrix and bf16 or fp32
-    activations X [T, K]: X is quantised as W was (the same rotation, the
-    channel scale divided out), then multiplied on the tensor cores."""
+    activations X [T, K] (qamw_mx4_linear): X is quantised as W was (the same
+    rotation, the channel scale divided out) into a workspace of its own, then
+    multiplied on the tensor cores. fp32 (default) or bf16 output."""
+    torch = _torch()
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    ot = _out_type(out_dtype)
+    device = _need_mx4("W", W)
     if W.divide:
         raise ValueError("W was quantised with divide=True: it is the activations' side of a product")
     _need_cuda("X", X, ndim=2)
-    if X.shape[1] != W.K:
+    if X.device != device:
+        raise ValueError(f"X must be on {device}, got {X.device}")
+    xt, ldx = _wdtype(X), _ld(X)
+    T, K = X.shape
+    if K != W.K:
         raise ValueError("X must have K columns")
-    with _on(W.codes, stream):
-        Xq = mx4_quantize(X, W.block, W.seed, W.col_scale, divide=True, status=status)
-        return mx4_matmul(W, Xq, out_dtype, status=status, out=out)
+    _need_status(device, status)
+    lib = load_library()
+    nws = ((T * (K // 2) + 255) & ~255) + mx4_scale_bytes(T, K)    # qamw_mx4_linear_workspace_bytes(T, K)
+    with _on(device, stream):
+        ws = torch.empty(nws, dtype=torch.uint8, device=device)
+        if out is None:
+            out, ld = torch.empty((T, W.M), dtype=out_dtype, device=device), W.M
+        else:
+            ld = _need_out("out", out, (T, W.M), out_dtype, device)
+        _check("qamw_mx4_linear", lib.qamw_mx4_linear(
+            W.codes.data_ptr(), W.scales.data_ptr(), W.M, X.data_ptr(), xt, T, K, ldx, _address(W.col_scale), W.block,
+            W.seed & (2**64 - 1), out.data_ptr(), ot, ld, ws.data_ptr(), nws, _address(status), _raw_stream(device)))
+    return out
 
 
 # ---------------------------------------------------------------------------
@@ -739,24 +789,29 @@ class _Head:
         torch = _torch()
         self.head, self.codebook, self.buffer = head, codebook, None
         self.coded = isinstance(head, (Encoded, Mx4))
-        if self.coded:
-            self.V, self.K = head.M, head.K
-            self.anchor = head.packed if isinstance(head, Encoded) else head.codes
-        else:
+        if not self.coded:
             _need_cuda("head", head, torch.bfloat16, 2)
             self.V, self.K = head.shape
-            self.anchor = head
-            _ld(head)
-        if isinstance(head, Encoded):
+            self.ld, self.device = _ld(head), head.device
+        elif isinstance(head, Mx4):
+            self.V, self.K, self.ld = head.M, head.K, head.K
+            self.device = _need_mx4("head", head)
+        else:
+            self.V, self.K, self.ld = head.M, head.K, head.K
             if codebook is None:
                 raise ValueError("an Encoded head needs its codebook")
             _need_cuda("codebook", codebook, torch.float32, 2)
-            _same_device(self.anchor, codebook=codebook, row_norm=head.row_norm, sigma=head.sigma,
+            _need_cuda("head.packed", head.packed, torch.int32, 2)
+            self.device = head.packed.device
+            _same_device(self.device, codebook=codebook, row_norm=head.row_norm, sigma=head.sigma,
                          col_scale=head.col_scale)
-            if head.packed.shape[0] != head.M or not head.packed.is_contiguous():
-                raise ValueError("head.packed must be contiguous with a row per vocabulary entry")
-        elif isinstance(head, Mx4):
-            _need_mx4("head", head)
+            if head.packed.shape != (head.M, words_per_row(head.K, head.bits)) or not head.packed.is_contiguous():
+                raise ValueError("head.packed must be contiguous [M, words_per_row(K, bits)]")
+            _need_cuda("head.row_norm", head.row_norm, torch.float32, 1)
+            _need_cuda("head.sigma", head.sigma, torch.float32, 1)
+            if head.row_norm.shape[0] != head.M or head.sigma.shape[0] != head.K // 2:
+                raise ValueError("head.row_norm and head.sigma must be [M] and [K/2]")
+            _need_scale(self.device, head.col_scale, head.K)
 
     def rows(self, v0: int, n: int, status):
         h = self.head
@@ -764,7 +819,7 @@ class _Head:
             return h[v0:v0 + n]
         torch = _torch()
         if self.buffer is None:
-            self.buffer = torch.empty((n, self.K), dtype=torch.bfloat16, device=self.anchor.device)
+            self.buffer = torch.empty((n, self.K), dtype=torch.bfloat16, device=self.device)
         out = self.buffer[:n]
         if isinstance(h, Mx4):
             per = (self.K + 127) // 128 * 512       # scale bytes of a 128-row tile
@@ -789,21 +844,23 @@ def _ce_inputs(X, head, targets, codebook, status):
     _need_cuda("X", X, torch.bfloat16, 2)
     _need_cuda("targets", targets, torch.int64, 1)
     h = _Head(head, codebook)
-    _same_device(X, head=h.anchor, targets=targets)
-    _need_status(X, status)
-    if X.shape[1] != h.K:
-        raise ValueError(f"X has {X.shape[1]} columns and the head {h.K}")
-    if targets.shape[0] != X.shape[0]:
+    device = X.device
+    if h.device != device or targets.device != device:
+        raise ValueError(f"head and targets must be on {device}")
+    _need_status(device, status)
+    T, K = X.shape
+    if K != h.K:
+        raise ValueError(f"X has {K} columns and the head {h.K}")
+    if targets.shape[0] != T:
         raise ValueError("targets must have one entry per row of X")
-    if targets.shape[0] > 1 and targets.stride(0) != 1:
+    if T > 1 and targets.stride(0) != 1:
         raise ValueError("targets must be contiguous")
-    return h, _ld(X)
+    return h, _ld(X), device
 
 
-def _need_rows(name, t, T, first):
-    torch = _torch()
-    _need_cuda(name, t, torch.float32, 1)
-    _same_device(first, **{name: t})
+def _need_rows(name, t, T, device):
+    _need_cuda(name, t, _torch().float32, 1)
+    _same_device(device, **{name: t})
     if t.shape[0] != T or (T > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be contiguous float32 [{T}]")
 
@@ -815,22 +872,23 @@ def cross_entropy(X, head, targets, codebook=None, ignore_index: int = -100, pie
     ``codebook``) or an :class:`Mx4`; coded heads are decoded to bf16 ``piece``
     rows at a time. ``targets`` is int64 [T]; ``ignore_index`` has loss 0."""
     torch = _torch()
-    h, ldx = _ce_inputs(X, head, targets, codebook, status)
+    h, ldx, device = _ce_inputs(X, head, targets, codebook, status)
     T, lib = X.shape[0], load_library()
     rows = _piece_rows(h.V, piece, _DECODED_BYTES // (2 * h.K) if h.coded else h.V + VOCAB_TILE)
-    with _on(X, stream):
+    with _on(device, stream):
         nws = int(lib.qamw_cross_entropy_workspace_bytes(T, h.V))
-        ws = torch.empty(nws, dtype=torch.uint8, device=X.device)
-        loss = torch.empty(T, dtype=torch.float32, device=X.device)
-        lse = torch.empty(T, dtype=torch.float32, device=X.device)
+        ws = torch.empty(nws, dtype=torch.uint8, device=device)
+        loss = torch.empty(T, dtype=torch.float32, device=device)
+        lse = torch.empty(T, dtype=torch.float32, device=device)
+        at, st, rs = targets.data_ptr(), _address(status), _raw_stream(device)
         for v0 in range(0, h.V, rows):
             n = min(rows, h.V - v0)
             W = h.rows(v0, n, status)
             _check("qamw_cross_entropy_piece", lib.qamw_cross_entropy_piece(
-                _ptr(X), T, h.K, ldx, _ptr(W), n, _ld(W), v0, h.V, _ptr(targets), ignore_index, _ptr(ws), nws,
-                _ptr(status), _stream_ptr()))
+                X.data_ptr(), T, h.K, ldx, W.data_ptr(), n, h.ld, v0, h.V, at, ignore_index, ws.data_ptr(), nws, st,
+                rs))
         _check("qamw_cross_entropy_finish", lib.qamw_cross_entropy_finish(
-            T, h.V, _ptr(targets), ignore_index, _ptr(ws), nws, _ptr(loss), _ptr(lse), _ptr(status), _stream_ptr()))
+            T, h.V, at, ignore_index, ws.data_ptr(), nws, loss.data_ptr(), lse.data_ptr(), st, rs))
     return loss, lse
 
 
@@ -843,28 +901,29 @@ def cross_entropy_grad(X, head, targets, lse, grad_loss, codebook=None, ignore_i
     ``weight_grad`` says otherwise. The logits are formed again, ``piece``
     vocabulary entries at a time."""
     torch = _torch()
-    h, ldx = _ce_inputs(X, head, targets, codebook, status)
+    h, ldx, device = _ce_inputs(X, head, targets, codebook, status)
     T, lib = X.shape[0], load_library()
-    _need_rows("lse", lse, T, X)
-    _need_rows("grad_loss", grad_loss, T, X)
+    _need_rows("lse", lse, T, device)
+    _need_rows("grad_loss", grad_loss, T, device)
     rows = _piece_rows(h.V, piece, min(_GRAD_BYTES // (2 * max(T, 1)),
                                        _DECODED_BYTES // (2 * h.K) if h.coded else h.V + VOCAB_TILE))
     if weight_grad is None:
         weight_grad = not h.coded
-    with _on(X, stream):
+    with _on(device, stream):
         nws = int(lib.qamw_cross_entropy_grad_workspace_bytes(T, h.K, rows))
-        ws = torch.empty(nws, dtype=torch.uint8, device=X.device)
-        dX = torch.empty((T, h.K), dtype=torch.bfloat16, device=X.device)
-        dW = torch.empty((h.V, h.K), dtype=torch.bfloat16, device=X.device) if weight_grad else None
+        ws = torch.empty(nws, dtype=torch.uint8, device=device)
+        dX = torch.empty((T, h.K), dtype=torch.bfloat16, device=device)
+        dW = torch.empty((h.V, h.K), dtype=torch.bfloat16, device=device) if weight_grad else None
+        at, st, rs = targets.data_ptr(), _address(status), _raw_stream(device)
         for v0 in range(0, h.V, rows):
             n = min(rows, h.V - v0)
             W = h.rows(v0, n, status)
             _check("qamw_cross_entropy_grad_piece", lib.qamw_cross_entropy_grad_piece(
-                _ptr(X), T, h.K, ldx, _ptr(W), n, _ld(W), v0, h.V, _ptr(targets), ignore_index, _ptr(lse),
-                _ptr(grad_loss), rows, int(v0 == 0), _ptr(dW[v0:v0 + n] if weight_grad else None), h.K, _ptr(ws), nws,
-                _ptr(status), _stream_ptr()))
+                X.data_ptr(), T, h.K, ldx, W.data_ptr(), n, h.ld, v0, h.V, at, ignore_index, lse.data_ptr(),
+                grad_loss.data_ptr(), rows, int(v0 == 0), _address(dW[v0:v0 + n] if weight_grad else None), h.K,
+                ws.data_ptr(), nws, st, rs))
         _check("qamw_cross_entropy_grad_finish", lib.qamw_cross_entropy_grad_finish(
-            T, h.K, rows, _ptr(dX), h.K, _ptr(ws), nws, _stream_ptr()))
+            T, h.K, rows, dX.data_ptr(), h.K, ws.data_ptr(), nws, rs))
     return dX, dW
 
 

@@ -733,6 +733,44 @@ int qamw_mx4_matmul(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, 
   return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
 }
 
+size_t qamw_mx4_linear_workspace_bytes(int64_t T, int64_t K) {
+  const size_t scales = qamw_mx4_scale_bytes(T, K);
+  return scales == 0 ? 0 : align256((size_t)T * (size_t)(K / 2)) + scales;
+}
+
+int qamw_mx4_linear(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, const void *X, qamw_dtype x_dtype,
+                    int64_t T, int64_t K, int64_t ldx, const float *col_scale, int32_t block, uint64_t sign_seed,
+                    void *Y, qamw_dtype out_dtype, int64_t ldy, void *workspace, size_t workspace_bytes,
+                    int32_t *status, qamw_stream_t stream) {
+  static const char *fn = "qamw_mx4_linear";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  if (!X || !Y) return fail(QAMW_ENULL, "%s: X and Y must be non-NULL", fn);
+  if ((rc = check_dtype(x_dtype, fn))) return rc;
+  if ((rc = check_dtype(out_dtype, fn))) return rc;
+  if ((rc = check_mx4(M, K, fn))) return rc;
+  if ((rc = check_mx4(T, K, fn))) return rc;
+  if ((rc = check_mx4_block(K, block, fn))) return rc;
+  if ((rc = check_mx4_codes(w_codes, w_scales, fn))) return rc;
+  if (ldx < K || ldy < M)
+    return fail(QAMW_EINVAL, "%s: ldx (%lld) must be >= K and ldy (%lld) >= M", fn, (long long)ldx, (long long)ldy);
+  if (!element_aligned(X, x_dtype) || !element_aligned(Y, out_dtype))
+    return fail(QAMW_EINVAL, "%s: X and Y must be aligned to their element sizes", fn);
+  const size_t need = qamw_mx4_linear_workspace_bytes(T, K);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(QAMW_EWORKSPACE, "%s: workspace of %zu bytes needed (got %zu)", fn, need, workspace_bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(QAMW_EINVAL, "%s: workspace must be 256-byte aligned", fn);
+  uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + align256((size_t)T * (size_t)(K / 2));
+  Mx4QuantizeArgs q{X, x_dtype, T, K, ldx, col_scale, 1, block ? log2i(block) : 0, sign_seed, codes, scales, status};
+  cudaError_t e = launch_mx4_quantize(q, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  Mx4MatmulArgs a{w_codes, w_scales, M, codes, scales, T, K, Y, out_dtype, ldy, status};
+  e = launch_mx4_matmul(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
 // Checks shared by the cross entropy's entry points.
 static int check_ce_sizes(int64_t T, int64_t K, int64_t V, const char *fn) {
   if (T < 1 || T > (int64_t(1) << 24)) return fail(QAMW_EINVAL, "%s: T must be in [1, 2^24] (got %lld)", fn, (long long)T);
