@@ -20,14 +20,16 @@
 // Error of the fp32 value, with A = sum of |v| over the block: v itself 2 x
 // 2^-24 (1/s rounded, and the product), one rounding of at most 2^-24 A per
 // butterfly level, the factor 2^-e / sqrt(b) and its product 2 x 2^-24, and the
-// sum y +- m one more: (log2 b + 6) 2^-24 A, with one 2^-24 A for the error of A.
+// sum y +- m one more: (log2 b + 5) 2^-24 A. A <= sqrt(b sum v^2) takes its
+// place: half the instructions, 1.25 times as large for Gaussian rows. The
+// factor is log2 b + 8 for the roundings of the bound itself.
 //
 // A lane loads two runs of 16 columns, 64 columns apart, so that four lanes
 // read 128 contiguous bytes of bf16; block bits 0-3 and 6 are butterflies on
-// its registers. An exchange of half the registers with the neighbour lane
-// swaps column bits 4 and 6: then the lane holds one whole group of 32 columns,
-// bit 4 is a register butterfly too, the group's maximum needs no exchange and
-// its codes are one 16-byte store. Bit 5 and bits 7-9 are lane exchanges.
+// its registers (two columns an instruction), bits 4, 5 and 7-9 exchanges
+// between lanes. A group of 32 columns is one run of two neighbour lanes.
+#include <type_traits>
+
 #include <cuda_fp16.h>
 
 #include "qamw_device.cuh"
@@ -36,7 +38,12 @@
 namespace qamw {
 namespace {
 
-constexpr int kMxWarps = 8;         // warps per CTA
+constexpr int kMxWarps = 4;         // warps per CTA
+// Warps that an SM is meant to hold: 16 (128 registers) for the quantisation of
+// prepared rows (11008 x 4096 bf16, b = 128: 71 us; 20 warps the same, 24 spill: 84),
+// 24 for the kernels without the error bound (values of the same matrix
+// decoded: 29 us at 16, 27 at 24).
+constexpr int kMxResident = 16, kMxResidentPlain = 24;
 constexpr int kMxUnit = 1024;       // columns per warp pass: 32 lanes x 32 columns
 
 // Byte offset of the scale of (row, group) in the tiled layout: tiles of 128
@@ -181,97 +188,93 @@ __device__ __forceinline__ void load16(const T *p, int vec, bool in, uint32_t *w
   }
 }
 
-// one fp64 value of the prepared row: y_col = sum_i (-1)^popc(i & col) d_i v_i / sqrt(b)
-// over the columns i of its block, formed by the whole warp
+// What decide_exactly found: code words and the masks of the codes decided.
+struct Decided {
+  uint32_t code[4], mask[4];
+  int e;
+  bool finite;
+};
+
+// A group's 32 values in fp64, lane k forming y of its column k: the block's
+// v_i are loaded once, 32 at a time, and handed round,
+//   y_k = sum_i (-1)^popc(i & k) d_i v_i / sqrt(b).
+// Then the codes of the values of `mask` at the exponent e; with all of them
+// (mask ~0) the group's exponent is found too. Warp-collective.
 template <typename T>
-__device__ __noinline__ double exact_value(const MxQuantArgs &p, int64_t row, int64_t col) {
+__device__ __noinline__ Decided decide_exactly(const MxQuantArgs &p, int64_t row, int64_t group, uint32_t mask, int e) {
   const int lane = threadIdx.x & 31, b = 1 << p.log2b;
-  const int64_t base = col & ~(int64_t)(b - 1);
+  const int64_t base = (32 * group) & ~(int64_t)((b > 32 ? b : 32) - 1);
+  const int local = (int)(32 * group - base);            // of the group in its block (0 for b <= 32)
   const void *w = static_cast<const T *>(p.W) + row * p.ldw;
-  double y = 0.0;
-  for (int i = lane; i < b; i += 32) {
-    const int64_t c = base + i;
+  uint32_t flip = 0;                                      // bit i: the sign of v_i in y_lane
+  for (int i = 0; i < 32; ++i) flip |= (uint32_t)(__popc(i & lane & (b - 1)) & 1) << i;
+  double y0 = 0.0, y1 = 0.0;
+  for (int q = 0; q < (b > 32 ? b : 32); q += 32) {
+    const int64_t c = base + q + lane;
     double v = Raw<T>::exact(w, c);
     if (p.s != nullptr) v = p.divide ? v / (double)p.s[c] : v * (double)p.s[c];
-    if (p.log2b > 0 && (mask_is_negative(p.seed, c) != ((__popc(i & (int)(col - base)) & 1) != 0))) v = -v;
-    y += v;
+    if (p.log2b > 0 && mask_is_negative(p.seed, c)) v = -v;
+    const uint32_t f = (__popc(q & local) & 1) ? ~flip : flip;
+    if (b >= 32) {
+#pragma unroll 8
+      for (int i = 0; i < 32; i += 2) {
+        const double s0 = __shfl_sync(0xffffffffu, v, i), s1 = __shfl_sync(0xffffffffu, v, i + 1);
+        y0 += ((f >> i) & 1u) ? -s0 : s0;
+        y1 += ((f >> (i + 1)) & 1u) ? -s1 : s1;
+      }
+    } else {                                              // several blocks in a group: the lane's own
+      for (int i = 0; i < 32; ++i) {
+        const double s0 = __shfl_sync(0xffffffffu, v, i);
+        if ((i >> p.log2b) == (lane >> p.log2b)) y0 += ((f >> i) & 1u) ? -s0 : s0;
+      }
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-  return p.log2b > 0 ? y * (1.0 / sqrt((double)b)) : y;
-}
-
-// Decides the values of `mask` of lane `src`'s group again, from fp64; with
-// all of them (mask ~0) the group's exponent too. Warp-collective.
-template <typename T>
-__device__ __noinline__ void decide_exactly(const MxQuantArgs &p, int64_t row, int64_t group, uint32_t mask, int src,
-                                            int &e, uint4 &codes, bool &finite) {
-  const int lane = threadIdx.x & 31;
-  double mine = 0.0;
-  for (uint32_t left = mask; left != 0u; left &= left - 1u) {
-    const int k = __ffs((int)left) - 1;
-    const double y = exact_value<T>(p, row, 32 * group + k);
-    if (lane == k) mine = y;
-  }
-  int ex = __shfl_sync(0xffffffffu, e, src);
-  bool fin = true;
+  double y = y0 + y1;
+  if (p.log2b > 0) y *= 1.0 / sqrt((double)b);
+  Decided d;
+  d.e = e;
+  d.finite = true;
   if (mask == 0xffffffffu) {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, (uint32_t)__double2hiint(mine) & 0x7FFFFFFFu);
-    fin = top < 0x7FF00000u;
-    ex = min(max((int)(top >> 20) - 1023 - 2, -127), 127);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, (uint32_t)__double2hiint(y) & 0x7FFFFFFFu);
+    d.finite = top < 0x7FF00000u;
+    d.e = min(max((int)(top >> 20) - 1023 - 2, -127), 127);
   }
-  const float pair[8] = {fin ? double_scaled(mine, ex) : 0.0f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const float one[8] = {d.finite ? double_scaled(y, d.e) : 0.0f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const bool own = (mask >> lane) & 1u;
-  uint32_t n = own ? (e2m1x8(pair) & 15u) << (4 * (lane & 7)) : 0u;     // this value's code, in its place
+  uint32_t n = own ? (e2m1x8(one) & 15u) << (4 * (lane & 7)) : 0u;     // this value's code, in its place
   uint32_t m = own ? 15u << (4 * (lane & 7)) : 0u;
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
     n |= __shfl_xor_sync(0xffffffffu, n, o);
     m |= __shfl_xor_sync(0xffffffffu, m, o);
   }
-  uint32_t nw[4], mw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    nw[i] = __shfl_sync(0xffffffffu, n, 8 * i);
-    mw[i] = __shfl_sync(0xffffffffu, m, 8 * i);
+    d.code[i] = __shfl_sync(0xffffffffu, n, 8 * i);
+    d.mask[i] = __shfl_sync(0xffffffffu, m, 8 * i);
   }
-  if (lane == src) {
-    codes.x = (codes.x & ~mw[0]) | nw[0];
-    codes.y = (codes.y & ~mw[1]) | nw[1];
-    codes.z = (codes.z & ~mw[2]) | nw[2];
-    codes.w = (codes.w & ~mw[3]) | nw[3];
-    e = ex;
-    finite = fin;
-  }
+  return d;
 }
 
-// The lane's place in a unit of 1024 columns: column bits 4 and 5 of its loads
-// are lane bits 0 and 1, bit 6 its two runs, bits 7-9 lane bits 2-4.
+// The lane's place in a unit of 1024 columns: column bits 4 and 5 are lane bits
+// 0 and 1, bit 6 its two runs, bits 7-9 lane bits 2-4.
 struct LanePlace {
   int64_t run0;    // first column of run 0; run 1 starts 64 columns on
-  int64_t group;   // the group that it holds after the exchange
-  int sub;         // that group's place among the four of its scale word
+  int64_t group0;  // the group of run 0; run 1's is the second next
   __device__ __forceinline__ LanePlace(int64_t unit, int lane) {
-    const int64_t sb = unit * kMxUnit + 128 * (lane >> 2);
-    run0 = sb + 32 * ((lane >> 1) & 1) + 16 * (lane & 1);
-    sub = 2 * (lane & 1) + ((lane >> 1) & 1);
-    group = sb / 32 + sub;
+    run0 = unit * kMxUnit + 128 * (lane >> 2) + 32 * ((lane >> 1) & 1) + 16 * (lane & 1);
+    group0 = run0 / 32;
   }
 };
 
-// x[j] = (run 0, run 1) of column j  ->  y[j] = columns (j, j + 16) of the
-// lane's group (to_group), or back: lane bit 0 and the run trade places.
-__device__ __forceinline__ void exchange(float2 (&x)[16], int lane) {
-  const bool odd = (lane & 1) != 0;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? x[j].x : x[j].y, 1);
-    if (odd) x[j].x = got;
-    else x[j].y = got;
-  }
-}
-
 __device__ __forceinline__ float2 diff2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
+
+// the largest magnitude of three (NaNs left out)
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // block bits 0-3: column bits 0-3 are the index j of the array
 __device__ __forceinline__ void butterflies_low(float2 (&x)[16], int log2b) {
@@ -305,54 +308,67 @@ __device__ __forceinline__ void butterflies_lane(float2 (&x)[16], int lane, int 
   }
 }
 
-// Signed column factors of the lane's 2 x 16 loaded columns: +-s, +-1/s or +-1.
-// A factor far from 1 becomes NaN: its rows are then decided from fp64.
-__device__ __forceinline__ void column_factors(const float *s, int divide, int log2b, uint64_t seed, int64_t run0,
-                                               int64_t K, float2 (&f)[16]) {
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int64_t col = run0 + 64 * c + j;
-      float v = 1.0f;
-      if (col < K) {
-        if (s != nullptr) {
-          v = divide ? __frcp_rn(s[col]) : s[col];
-          if (!(fabsf(v) > 0x1p-100f && fabsf(v) < 0x1p100f)) v = __uint_as_float(0x7FC00000u);
-        }
-        if (log2b > 0 && mask_is_negative(seed, col)) v = -v;
-      }
-      if (c == 0) f[j].x = v;
-      else f[j].y = v;
-    }
+// Column factors of a unit, formed once by the CTA (its warps work on rows of
+// one unit) and kept in shared memory as the lanes read them: 8 x 32 float4,
+// (run 0, run 1) of columns 2i and 2i + 1 of a lane.
+using Factors = float4[8][32];
+__device__ __forceinline__ float2 factor(const Factors &f, int lane, int j) {
+  const float4 q = f[j >> 1][lane];
+  return (j & 1) ? make_float2(q.z, q.w) : make_float2(q.x, q.y);
+}
+template <typename F>
+__device__ __forceinline__ void form_factors(Factors &f, int64_t unit, int64_t K, F of) {
+  for (int i = threadIdx.x; i < kMxUnit; i += blockDim.x) {
+    const int64_t col = unit * kMxUnit + i;
+    const int lane = 4 * (i >> 7) + ((i >> 4) & 3), j = i & 15, run = (i >> 6) & 1;
+    reinterpret_cast<float *>(&f[j >> 1][lane])[2 * (j & 1) + run] = col < K ? of(col) : 1.0f;
   }
+  __syncthreads();
 }
 
-// PREP: a channel scale or a rotation; otherwise the values are exact as read.
-template <typename T, bool PREP>
-__global__ void __launch_bounds__(32 * kMxWarps) mx4_quantize_kernel(MxQuantArgs p) {
+// Every butterfly of a block of 2^LB columns on the lane's 2 x 16 columns.
+template <int LB>
+__device__ __forceinline__ void rotate(float2 (&x)[16], int lane) {
+  butterflies_low(x, LB);
+  if constexpr (LB > 6) butterflies_pair(x);
+  if constexpr (LB > 4) butterflies_lane(x, lane, 1);
+  if constexpr (LB > 5) butterflies_lane(x, lane, 2);
+#pragma unroll
+  for (int t = 7; t < LB; ++t) butterflies_lane(x, lane, 1 << (t - 5));
+}
+
+// PREP: a channel scale or a rotation (blocks of 2^LB columns); otherwise the
+// values are exact as read.
+template <typename T, bool PREP, int LB>
+__global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxResidentPlain) / kMxWarps)
+    mx4_quantize_kernel(const __grid_constant__ MxQuantArgs p) {
   constexpr int N = Raw<T>::kWords;
   const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * kMxWarps + (threadIdx.x >> 5);
-  if (id >= p.units_k * p.row_groups) return;
-  const int64_t unit = id % p.units_k, rg = id / p.units_k;
+  const int64_t unit = blockIdx.x % p.units_k, rg = (blockIdx.x / p.units_k) * kMxWarps + (threadIdx.x >> 5);
   const LanePlace at(unit, lane);
   const int64_t k_tiles = (p.K + 127) / 128, rows_pad = (p.M + 127) / 128 * 128;
   // K % 32 == 0: a run of 16 columns and a group are all in or all out
-  const bool in0 = at.run0 < p.K, in1 = at.run0 + 64 < p.K, in = 32 * at.group < p.K;
+  const bool in[2] = {at.run0 < p.K, at.run0 + 64 < p.K};
   const T *src = static_cast<const T *>(p.W) + at.run0;
-  float2 f[16];
-  if (PREP) column_factors(p.s, p.divide, p.log2b, p.seed, at.run0, p.K, f);
-  const float inv = (float)(1.0 / sqrt((double)(1 << p.log2b)));
-  const float bound = (float)(p.log2b + 7) * 0x1p-24f;
+  __shared__ Factors f;
+  if (PREP)   // +-s, +-1/s or +-1; one far from 1 becomes NaN: its rows are decided from fp64
+    form_factors(f, unit, p.K, [&](int64_t col) {
+      float v = 1.0f;
+      if (p.s != nullptr) {
+        v = p.divide ? __frcp_rn(p.s[col]) : p.s[col];
+        if (!(fabsf(v) > 0x1p-100f && fabsf(v) < 0x1p100f)) v = __uint_as_float(0x7FC00000u);
+      }
+      return (LB > 0 && mask_is_negative(p.seed, col)) ? -v : v;
+    });
+  const float inv = (float)(1.0 / sqrt((double)(1 << LB)));
   uint32_t bad = 0;
   uint32_t w0[N], w1[N];
   if (rg < p.M) {
-    load16<T>(src + rg * p.ldw, p.vec, in0, w0);
-    load16<T>(src + rg * p.ldw + 64, p.vec, in1, w1);
+    load16<T>(src + rg * p.ldw, p.vec, in[0], w0);
+    load16<T>(src + rg * p.ldw + 64, p.vec, in[1], w1);
   }
   for (int64_t row = rg; row < rows_pad; row += p.row_groups) {
-    uint32_t sbyte = 0;
+    uint32_t sword = 0;
     if (row < p.M) {
       float2 x[16];
 #pragma unroll
@@ -361,113 +377,138 @@ __global__ void __launch_bounds__(32 * kMxWarps) mx4_quantize_kernel(MxQuantArgs
       if (PREP) {
         const uint32_t drop = N == 8 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
 #pragma unroll
-        for (int i = 0; i < N; ++i) any0 |= w0[i] & drop, any1 |= w1[i] & drop;
+        for (int i = 0; i < N; ++i) any0 |= w0[i], any1 |= w1[i];
+        any0 &= drop;
+        any1 &= drop;
       }
       const int64_t next = row + p.row_groups;
       if (next < p.M) {               // the next row is on its way while this one is worked on
-        load16<T>(src + next * p.ldw, p.vec, in0, w0);
-        load16<T>(src + next * p.ldw + 64, p.vec, in1, w1);
+        load16<T>(src + next * p.ldw, p.vec, in[0], w0);
+        load16<T>(src + next * p.ldw + 64, p.vec, in[1], w1);
       }
-      int e = -127;
-      bool finite = true;
-      uint4 c = make_uint4(0u, 0u, 0u, 0u);
+      int e[2] = {-127, -127};
+      bool finite[2] = {true, true};
+      uint32_t c[2][2] = {{0u, 0u}, {0u, 0u}};
       if (PREP) {
-        float2 sum = make_float2(any0 ? 0x1p-120f : 0.0f, any1 ? 0x1p-120f : 0.0f);   // |v| of each run; 0: a run of zeros
+        // sum of v^2 over the group's block (the group itself for smaller blocks); 0: nothing but zeros
+        float2 q = make_float2(any0 ? 0x1p-120f : 0.0f, any1 ? 0x1p-120f : 0.0f);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          x[j] = mul2(x[j], f[j]);
-          sum = add2(sum, make_float2(fabsf(x[j].x), fabsf(x[j].y)));
+          x[j] = mul2(x[j], factor(f, lane, j));
+          q = fma2(x[j], x[j], q);
         }
-        // A over the group's block (the group itself for smaller blocks)
-        const bool odd = (lane & 1) != 0;
-        float A = (odd ? sum.y : sum.x) + __shfl_xor_sync(0xffffffffu, odd ? sum.x : sum.y, 1);
-        if (p.log2b > 5) A += __shfl_xor_sync(0xffffffffu, A, 2);
-        if (p.log2b > 6) A += __shfl_xor_sync(0xffffffffu, A, 1);
-        for (int t = 7; t < p.log2b; ++t) A += __shfl_xor_sync(0xffffffffu, A, 1 << (t - 5));
-        butterflies_low(x, p.log2b);
-        if (p.log2b > 6) butterflies_pair(x);
-        exchange(x, lane);
-        if (p.log2b > 4) butterflies_pair(x);
-        if (p.log2b > 5) butterflies_lane(x, lane, 2);
-        for (int t = 7; t < p.log2b; ++t) butterflies_lane(x, lane, 1 << (t - 5));
-        float top = 0.0f;
+        q = add2(q, make_float2(__shfl_xor_sync(0xffffffffu, q.x, 1), __shfl_xor_sync(0xffffffffu, q.y, 1)));
+        if (LB > 5) q = add2(q, make_float2(__shfl_xor_sync(0xffffffffu, q.x, 2), __shfl_xor_sync(0xffffffffu, q.y, 2)));
+        if (LB > 6) q.x = q.y = q.x + q.y;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) top = fmaxf(top, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
-        const float m = bound * A * inv;
-        const float lo = fmaxf(top * inv - m, 0.0f), hi = top * inv + m;
-        e = (int)(__float_as_uint(lo) >> 23) - 127 - 2;
-        uint32_t again = 0;           // the group's values to be decided from fp64
-        if (in && A != 0.0f) {
-          const bool sure = A > 0x1p-90f && A < 0x1p90f && (__float_as_uint(lo) >> 23) == (__float_as_uint(hi) >> 23);
-          if (sure) {
-            const float scale = inv * __uint_as_float((uint32_t)(127 - e) << 23), ms = m * __uint_as_float((uint32_t)(127 - e) << 23);
-            float u[16], v[16];
-            uint32_t cw[4];
+        for (int t = 7; t < LB; ++t) q.x = q.y = q.x + __shfl_xor_sync(0xffffffffu, q.x, 1 << (t - 5));
+        rotate<LB>(x, lane);
+        float2 top = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+        for (int j = 0; j < 16; j += 2)
+          top = make_float2(max_abs(top.x, x[j].x, x[j + 1].x), max_abs(top.y, x[j].y, x[j + 1].y));
+        top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, 1));
+        top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, 1));
+        constexpr float kBound = (float)(LB + 8) * 0x1p-24f;
+        constexpr float kTerms = (float)(1 << (LB > 5 ? LB : 5));
+        float2 scale, ms;             // 2^-e / sqrt(b) and m 2^-e of each run
+        uint32_t again[2] = {0u, 0u}; // the run's values to be decided from fp64
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float t = h ? x[j].y : x[j].x;
-                u[j] = __fmaf_rn(t, scale, -ms);
-                v[j] = __fmaf_rn(t, scale, ms);
-              }
+        for (int r = 0; r < 2; ++r) {
+          const float Q = r ? q.y : q.x, t = (r ? top.y : top.x) * inv;
+          const float m = kBound * inv * sqrtf(kTerms * Q);
+          const float lo = fmaxf(t - m, 0.0f), hi = t + m;
+          e[r] = (int)(__float_as_uint(lo) >> 23) - 127 - 2;
+          const bool zero = Q == 0.0f || !in[r];
+          const bool sure = Q > 0x1p-100f && Q < 0x1p100f && (__float_as_uint(lo) >> 23) == (__float_as_uint(hi) >> 23);
+          if (!sure) e[r] = -127;
+          if (!sure && !zero) again[r] = 0xffffu;
+          const float up = sure ? __uint_as_float((uint32_t)(127 - e[r]) << 23) : 0.0f;   // !sure: codes 0 for now
+          (r ? scale.y : scale.x) = inv * up;
+          (r ? ms.y : ms.x) = sure ? m * up : 0.0f;
+        }
+        const float2 less = make_float2(-ms.x, -ms.y);
+        float u[2][16], v[2][16];
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const uint32_t a = e2m1x8(u + 8 * q), b = e2m1x8(v + 8 * q);
-                // a value within m of zero differs in its sign alone: it is +0
-                cw[2 * h + q] = a & b;
-                const uint32_t d = (a ^ b) & 0x77777777u;
-                if (d != 0u) {
+        for (int j = 0; j < 16; ++j) {
+          const float2 a = fma2(x[j], scale, less), b = fma2(x[j], scale, ms);
+          u[0][j] = a.x, u[1][j] = a.y, v[0][j] = b.x, v[1][j] = b.y;
+        }
+        uint32_t open = again[0] | again[1];
+        uint32_t d[2][2];
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if ((d >> (4 * i)) & 15u) again |= 1u << (16 * h + 8 * q + i);
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a = e2m1x8(u[r] + 8 * h), b = e2m1x8(v[r] + 8 * h);
+            c[r][h] = a & b;          // a value within m of zero differs in its sign alone: it is +0
+            d[r][h] = (a ^ b) & 0x77777777u;
+            open |= d[r][h];
+          }
+        }
+        if (__any_sync(0xffffffffu, open != 0u)) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if ((d[r][i >> 3] >> (4 * (i & 7))) & 15u) again[r] |= 1u << i;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, again[r], 1);
+            const uint32_t all = (lane & 1) ? (other | (again[r] << 16)) : (again[r] | (other << 16));
+            for (uint32_t lanes = __ballot_sync(0xffffffffu, all != 0u) & 0x55555555u; lanes != 0u;
+                 lanes &= lanes - 1u) {
+              const int l = __ffs((int)lanes) - 1;
+              const Decided n = decide_exactly<T>(p, row, __shfl_sync(0xffffffffu, at.group0, l) + 2 * r,
+                                                  __shfl_sync(0xffffffffu, all, l), __shfl_sync(0xffffffffu, e[r], l));
+              if ((lane & ~1) == l) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t code = (lane & 1) ? n.code[2 + h] : n.code[h];
+                  const uint32_t mask = (lane & 1) ? n.mask[2 + h] : n.mask[h];
+                  c[r][h] = (c[r][h] & ~mask) | code;
                 }
+                e[r] = n.e;
+                finite[r] = n.finite;
               }
             }
-            c = make_uint4(cw[0], cw[1], cw[2], cw[3]);
-          } else {
-            again = 0xffffffffu;
           }
-        } else {
-          e = -127;                   // nothing but zeros
-        }
-        for (uint32_t lanes = __ballot_sync(0xffffffffu, again != 0u); lanes != 0u; lanes &= lanes - 1u) {
-          const int l = __ffs((int)lanes) - 1;
-          decide_exactly<T>(p, row, __shfl_sync(0xffffffffu, at.group, l), __shfl_sync(0xffffffffu, again, l), l, e, c,
-                            finite);
         }
       } else {
-        exchange(x, lane);
-        uint32_t top = 0;
+        uint32_t top[2] = {0u, 0u};
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          top = max(top, __float_as_uint(x[j].x) & 0x7FFFFFFFu);
-          top = max(top, __float_as_uint(x[j].y) & 0x7FFFFFFFu);
+          top[0] = max(top[0], __float_as_uint(x[j].x) & 0x7FFFFFFFu);
+          top[1] = max(top[1], __float_as_uint(x[j].y) & 0x7FFFFFFFu);
         }
-        finite = top < 0x7F800000u;
-        e = max((int)(top >> 23) - 127 - 2, -127);   // a subnormal maximum: -127
-        // 2^-e is a normal float for every e in -127 .. 125
-        const float scale = __uint_as_float((uint32_t)(127 - e) << 23);
-        float u[16], v[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) u[j] = __fmul_rn(x[j].x, scale), v[j] = __fmul_rn(x[j].y, scale);
-        c = make_uint4(e2m1x8(u), e2m1x8(u + 8), e2m1x8(v), e2m1x8(v + 8));
-      }
-      if (in) {
-        if (!finite) {
-          c = make_uint4(0u, 0u, 0u, 0u);
-          bad |= QAMW_STATUS_NONFINITE_INPUT;
+        for (int r = 0; r < 2; ++r) {
+          top[r] = max(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+          finite[r] = top[r] < 0x7F800000u;
+          e[r] = max((int)(top[r] >> 23) - 127 - 2, -127);   // a subnormal maximum: -127
+          // 2^-e is a normal float for every e in -127 .. 125
+          const float up = __uint_as_float((uint32_t)(127 - e[r]) << 23);
+          float u[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) u[j] = __fmul_rn(r ? x[j].y : x[j].x, up);
+          c[r][0] = e2m1x8(u);
+          c[r][1] = e2m1x8(u + 8);
         }
-        sbyte = finite ? (uint32_t)(e + 127) : 255u;
-        *reinterpret_cast<uint4 *>(p.codes + row * (p.K / 2) + 16 * at.group) = c;
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (in[r]) {
+          if (!finite[r]) {
+            c[r][0] = c[r][1] = 0u;
+            bad |= QAMW_STATUS_NONFINITE_INPUT;
+          }
+          // the two groups of this lane's scale word: bytes (lane bit 1) and 2 + (lane bit 1)
+          sword |= (finite[r] ? (uint32_t)(e[r] + 127) : 255u) << (16 * r + 4 * (lane & 2));
+          *reinterpret_cast<uint2 *>(p.codes + row * (p.K / 2) + at.run0 / 2 + 32 * r) = make_uint2(c[r][0], c[r][1]);
+        }
       }
     }
-    // four lanes' scale bytes form one word of a tile
-    uint32_t w = sbyte << (8 * at.sub);
-    w |= __shfl_xor_sync(0xffffffffu, w, 1);
-    w |= __shfl_xor_sync(0xffffffffu, w, 2);
-    if ((lane & 3) == 0 && at.group / 4 < k_tiles)
-      *reinterpret_cast<uint32_t *>(p.scales + scale_offset(row, at.group, k_tiles)) = w;
+    sword |= __shfl_xor_sync(0xffffffffu, sword, 2);
+    if ((lane & 3) == 0 && at.group0 / 4 < k_tiles)
+      *reinterpret_cast<uint32_t *>(p.scales + scale_offset(row, at.group0, k_tiles)) = sword;
   }
   bad = __reduce_or_sync(0xffffffffu, bad);
   if (lane == 0) status_or(p.status, bad);
@@ -518,64 +559,50 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *p, int vec, const float (
 
 // x = d (.) (H_b q 2^e) / (sqrt(b) s) (times s for divided rows): fp32
 // arithmetic, one rounding to the output type, like the codec's own decode.
-// Without a rotation and a scale every value is exact in either type. The
-// lane's group of 32 columns goes the quantisation's way back: pairs and lane
-// exchanges, the exchange of runs, then the bits of a run, and the column
-// factor d / (sqrt(b) s), formed once for all rows of the warp.
-template <typename T>
-__global__ void __launch_bounds__(32 * kMxWarps) mx4_decode_kernel(MxDecodeArgs p) {
+// Without a rotation and a scale every value is exact in either type. Lanes
+// hold what they hold in the quantisation; the column factor d / (sqrt(b) s) is
+// formed once for all rows of the warp.
+template <typename T, int LB>
+__global__ void __launch_bounds__(32 * kMxWarps, kMxResidentPlain / kMxWarps) mx4_decode_kernel(const __grid_constant__ MxDecodeArgs p) {
   const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * kMxWarps + (threadIdx.x >> 5);
-  if (id >= p.units_k * p.row_groups) return;
-  const int64_t unit = id % p.units_k, rg = id / p.units_k;
+  const int64_t unit = blockIdx.x % p.units_k, rg = (blockIdx.x / p.units_k) * kMxWarps + (threadIdx.x >> 5);
   const LanePlace at(unit, lane);
   const int64_t k_tiles = (p.K + 127) / 128;
-  const bool in0 = at.run0 < p.K, in1 = at.run0 + 64 < p.K, in = 32 * at.group < p.K;
-  const float inv = (float)(1.0 / sqrt((double)(1 << p.log2b)));
-  float2 f[16];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int64_t col = at.run0 + 64 * c + j;
-      float v = inv;
-      if (col < p.K) {
-        if (p.s != nullptr) v = p.divide ? __fmul_rn(inv, p.s[col]) : __fdiv_rn(inv, p.s[col]);
-        if (p.log2b > 0 && mask_is_negative(p.seed, col)) v = -v;
-      }
-      if (c == 0) f[j].x = v;
-      else f[j].y = v;
-    }
-  }
-  uint4 c = make_uint4(0u, 0u, 0u, 0u);
-  uint32_t sb = 0;
+  const bool in0 = at.run0 < p.K, in1 = at.run0 + 64 < p.K;
+  const float inv = (float)(1.0 / sqrt((double)(1 << LB)));
+  __shared__ Factors f;
+  form_factors(f, unit, p.K, [&](int64_t col) {
+    float v = inv;
+    if (p.s != nullptr) v = p.divide ? __fmul_rn(inv, p.s[col]) : __fdiv_rn(inv, p.s[col]);
+    return (LB > 0 && mask_is_negative(p.seed, col)) ? -v : v;
+  });
+  uint2 c0 = make_uint2(0u, 0u), c1 = make_uint2(0u, 0u);
+  uint32_t sw = 0;                    // the scale bytes of four groups, two of them this lane's
   auto fetch = [&](int64_t row) {
-    if (in) {
-      c = *reinterpret_cast<const uint4 *>(p.codes + row * (p.K / 2) + 16 * at.group);
-      sb = p.scales[scale_offset(row, at.group, k_tiles)];
+    const uint8_t *q = p.codes + row * (p.K / 2) + at.run0 / 2;
+    if (in0) {
+      c0 = *reinterpret_cast<const uint2 *>(q);
+      sw = *reinterpret_cast<const uint32_t *>(p.scales + scale_offset(row, at.group0 & ~(int64_t)3, k_tiles));
     }
+    if (in1) c1 = *reinterpret_cast<const uint2 *>(q + 32);
   };
   if (rg < p.M) fetch(rg);
   for (int64_t row = rg; row < p.M; row += p.row_groups) {
     float u[16], v[16];
-    floats_of_e2m1x8(c.x, u);
-    floats_of_e2m1x8(c.y, u + 8);
-    floats_of_e2m1x8(c.z, v);
-    floats_of_e2m1x8(c.w, v + 8);
-    const float g = e8m0_value(sb);
+    floats_of_e2m1x8(c0.x, u);
+    floats_of_e2m1x8(c0.y, u + 8);
+    floats_of_e2m1x8(c1.x, v);
+    floats_of_e2m1x8(c1.y, v + 8);
+    const uint32_t sh = 4 * (lane & 2);
+    const float2 g = make_float2(e8m0_value((sw >> sh) & 255u), e8m0_value((sw >> (16 + sh)) & 255u));
     if (row + p.row_groups < p.M) fetch(row + p.row_groups);
     float2 x[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = make_float2(__fmul_rn(u[j], g), __fmul_rn(v[j], g));
-    for (int t = 7; t < p.log2b; ++t) butterflies_lane(x, lane, 1 << (t - 5));
-    if (p.log2b > 5) butterflies_lane(x, lane, 2);
-    if (p.log2b > 4) butterflies_pair(x);
-    exchange(x, lane);
-    if (p.log2b > 6) butterflies_pair(x);
-    butterflies_low(x, p.log2b);
+    for (int j = 0; j < 16; ++j) x[j] = mul2(make_float2(u[j], v[j]), g);
+    rotate<LB>(x, lane);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const float2 y = mul2(x[j], f[j]);
+      const float2 y = mul2(x[j], factor(f, lane, j));
       u[j] = y.x;
       v[j] = y.y;
     }
@@ -598,14 +625,31 @@ __global__ void mx4_scale_layout_kernel(const uint8_t *in, uint8_t *out, int64_t
   }
 }
 
-// Rows of one column unit are dealt out so that each warp has up to 16 rows
-// (the sign mask of its columns is formed once for all of them), as long as
-// enough warps remain to fill the GPU.
-int64_t row_groups_for(int64_t rows, int64_t units_k) {
-  const int64_t want = (int64_t)sm_count() * 16;            // warps that keep an SM busy
-  int64_t per = rows * units_k / want;
-  per = per < 1 ? 1 : per > 16 ? 16 : per;
-  return (rows + per - 1) / per;
+// Rows of one column unit are dealt out to as many warps as the GPU holds at
+// once (`resident` per SM), so that there is one wave and the column factors
+// are formed once for all rows of a CTA.
+int64_t row_groups_for(int64_t rows, int64_t units_k, int resident) {
+  const int64_t ctas = (int64_t)sm_count() * (resident / kMxWarps) / units_k, most = (rows + kMxWarps - 1) / kMxWarps;
+  return kMxWarps * (ctas < 1 ? 1 : ctas < most ? ctas : most);
+}
+
+// Calls f with log2 b as a compile-time constant: the butterflies of a block
+// are then straight code (every block size has its kernel).
+template <typename F>
+void with_log2b(int log2b, F f) {
+  switch (log2b) {
+    case 0: return f(std::integral_constant<int, 0>());
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 5: return f(std::integral_constant<int, 5>());
+    case 6: return f(std::integral_constant<int, 6>());
+    case 7: return f(std::integral_constant<int, 7>());
+    case 8: return f(std::integral_constant<int, 8>());
+    case 9: return f(std::integral_constant<int, 9>());
+    default: return f(std::integral_constant<int, 10>());
+  }
 }
 
 // the widest vector access (32, 16 or 0 bytes) that every row allows
@@ -632,16 +676,18 @@ cudaError_t launch_mx4_quantize(const Mx4QuantizeArgs &a, cudaStream_t s) {
   p.units_k = (a.K + kMxUnit - 1) / kMxUnit;
   const int es = a.wt == QAMW_BF16 ? 2 : 4;
   p.vec = vector_bytes(a.W, a.ldw * es);
-  p.row_groups = row_groups_for((a.M + 127) / 128 * 128, p.units_k);
-  const int64_t warps = p.units_k * p.row_groups;
-  const dim3 grid((unsigned)((warps + kMxWarps - 1) / kMxWarps));
-  const bool prep = a.col_scale != nullptr || a.log2b > 0;
-  if (a.wt == QAMW_BF16) {
-    if (prep) mx4_quantize_kernel<uint16_t, true><<<grid, 32 * kMxWarps, 0, s>>>(p);
-    else mx4_quantize_kernel<uint16_t, false><<<grid, 32 * kMxWarps, 0, s>>>(p);
+  const bool plain = a.col_scale == nullptr && a.log2b == 0;
+  p.row_groups = row_groups_for((a.M + 127) / 128 * 128, p.units_k, plain ? kMxResidentPlain : kMxResident);
+  const dim3 grid((unsigned)(p.units_k * (p.row_groups / kMxWarps)));
+  auto run = [&](auto kernel) { kernel<<<grid, 32 * kMxWarps, 0, s>>>(p); };
+  if (plain) {
+    if (a.wt == QAMW_BF16) run(mx4_quantize_kernel<uint16_t, false, 0>);
+    else run(mx4_quantize_kernel<float, false, 0>);
   } else {
-    if (prep) mx4_quantize_kernel<float, true><<<grid, 32 * kMxWarps, 0, s>>>(p);
-    else mx4_quantize_kernel<float, false><<<grid, 32 * kMxWarps, 0, s>>>(p);
+    with_log2b(a.log2b, [&](auto lb) {
+      if (a.wt == QAMW_BF16) run(mx4_quantize_kernel<uint16_t, true, decltype(lb)::value>);
+      else run(mx4_quantize_kernel<float, true, decltype(lb)::value>);
+    });
   }
   return cudaGetLastError();
 }
@@ -661,11 +707,12 @@ cudaError_t launch_mx4_decode(const Mx4DecodeArgs &a, cudaStream_t s) {
   p.units_k = (a.K + kMxUnit - 1) / kMxUnit;
   const int es = a.out_t == QAMW_BF16 ? 2 : 4;
   p.vec = vector_bytes(a.out, a.ldo * es);
-  p.row_groups = row_groups_for(a.M, p.units_k);
-  const int64_t warps = p.units_k * p.row_groups;
-  const dim3 grid((unsigned)((warps + kMxWarps - 1) / kMxWarps));
-  if (a.out_t == QAMW_BF16) mx4_decode_kernel<__nv_bfloat16><<<grid, 32 * kMxWarps, 0, s>>>(p);
-  else mx4_decode_kernel<float><<<grid, 32 * kMxWarps, 0, s>>>(p);
+  p.row_groups = row_groups_for(a.M, p.units_k, kMxResidentPlain);
+  const dim3 grid((unsigned)(p.units_k * (p.row_groups / kMxWarps)));
+  with_log2b(a.log2b, [&](auto lb) {
+    if (a.out_t == QAMW_BF16) mx4_decode_kernel<__nv_bfloat16, decltype(lb)::value><<<grid, 32 * kMxWarps, 0, s>>>(p);
+    else mx4_decode_kernel<float, decltype(lb)::value><<<grid, 32 * kMxWarps, 0, s>>>(p);
+  });
   return cudaGetLastError();
 }
 
