@@ -766,7 +766,7 @@ int qamw_mx4_linear(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, 
   Mx4QuantizeArgs q{X, x_dtype, T, K, ldx, col_scale, 1, block ? log2i(block) : 0, sign_seed, codes, scales, status};
   cudaError_t e = launch_mx4_quantize(q, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, fn);
-  Mx4MatmulArgs a{w_codes, w_scales, M, codes, scales, T, K, Y, out_dtype, ldy, status};
+  Mx4MatmulArgs a{w_codes, w_scales, M, codes, scales, T, K, Y, out_dtype, ldy, status, 1};
   e = launch_mx4_matmul(a, (cudaStream_t)stream);
   return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
 }

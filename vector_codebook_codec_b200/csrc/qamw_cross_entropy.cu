@@ -61,20 +61,6 @@ struct CeTile {
   static constexpr int kStage = kA + kB;
 };
 
-__device__ __forceinline__ uint32_t cta_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
-  return r;
-}
-
 // Operand descriptor, 128-byte swizzle, rows (or columns) of the product
 // contiguous: a 64 x 64 box holds 64 contraction rows of 128 bytes; 8-row atoms
 // are 1024 bytes apart along the contraction, boxes 8192 bytes along the rows.
@@ -102,26 +88,14 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
 }
 template <int CTAS>
 __device__ __forceinline__ void commit(uint64_t *bar) {
-  if constexpr (CTAS == 1)
-    tc::commit(bar);
-  else   // to the barrier of both CTAs
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
+  if constexpr (CTAS == 1) tc::commit(bar);
+  else tc::commit_pair(bar);
 }
 template <int CTAS>
 __device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar,
                                          uint32_t leader_bar) {
-  if constexpr (CTAS == 1)
-    tc::load_2d(dst, map, x, y, bar);
-  else   // into this CTA's memory, counted at the leader's barrier
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-        "%3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(leader_bar)
-        : "memory");
+  if constexpr (CTAS == 1) tc::load_2d(dst, map, x, y, bar);
+  else tc::load_2d_pair(dst, map, x, y, leader_bar);
 }
 
 struct Unit {                     // one tile (and contraction range) of the walk
@@ -134,11 +108,7 @@ __device__ __forceinline__ Unit unit_of(const CeArgs &g, int64_t u) {
   const int64_t tiles = g.n_r * g.n_c;
   r.split = (int)(u / tiles);
   const int64_t t = u - r.split * tiles;
-  // groups of kGroupRows row tiles; inside a group the row varies fastest
-  const int64_t per = kGroupRows * g.n_c, grp = t / per, in = t - grp * per;
-  const int64_t left = g.n_r - grp * kGroupRows, h = left < kGroupRows ? left : kGroupRows;
-  r.ct = in / h;
-  r.rt = grp * kGroupRows + (in - r.ct * h);
+  tc::TileWalk{g.n_r, g.n_c, kGroupRows}.at(t, r.rt, r.ct);
   const int64_t all = (g.depth + kBK - 1) / kBK;
   r.k0 = r.split * g.steps_per_split;
   r.k1 = r.k0 + g.steps_per_split < all ? r.k0 + g.steps_per_split : all;
@@ -153,6 +123,7 @@ template <int CTAS, bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, CeArgs g) {
   using L = CeTile<CTAS>;
+  if constexpr (EPI == kStats) tc::griddep_launch_dependents();   // ce_finish_kernel, which waits for this one
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_slot;
@@ -160,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   volatile int *fail = &fail_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CTAS == 1 ? 0u : cta_rank();
+  const uint32_t rank = CTAS == 1 ? 0u : tc::cta_rank();
   const int S = g.stages;
   uint8_t *sA = smem, *sB = smem + (size_t)S * L::kA;
 
@@ -179,31 +150,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) {
     if constexpr (CTAS == 1) tc::alloc(&tmem_slot, 512);
-    else {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
-                   : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    }
+    else tc::alloc_pair(&tmem_slot, 512);
   }
   tc::fence_before();
   __syncthreads();
-  if constexpr (CTAS == 2) cluster_sync();   // both CTAs' barriers exist before either is signalled
+  if constexpr (CTAS == 2) tc::cluster_sync();   // both CTAs' barriers exist before either is signalled
   tc::fence_after();
   const uint32_t tmem = tmem_slot;
   const int64_t n_units = g.n_r * g.n_c * g.splits, step = gridDim.x / CTAS, first = blockIdx.x / CTAS;
   uint32_t bad = 0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int64_t u = first; u < n_units && ok; u += step) {
-        const Unit w = unit_of(g, u);
-        const int r0 = (int)(w.rt * L::kRows + rank * 128), c0 = (int)(w.ct * kBN + rank * L::kColsHere);
-        for (int64_t k = w.k0; k < w.k1; ++k, ++it) {
-          const uint32_t s = it % S;
-          if (!tc::wait(&empty[s], ((it / S) & 1u) ^ 1u, fail)) { ok = false; break; }
-          const uint32_t lb = CTAS == 1 ? 0u : leader_addr(&full[s]);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t u = first; u < n_units && ok; u += step) {
+      const Unit w = unit_of(g, u);
+      const int r0 = (int)(w.rt * L::kRows + rank * 128), c0 = (int)(w.ct * kBN + rank * L::kColsHere);
+      for (int64_t k = w.k0; k < w.k1; ++k, ++it) {
+        const uint32_t s = it % S;
+        if (!tc::wait(&empty[s], ((it / S) & 1u) ^ 1u, fail)) { ok = false; break; }
+        if (tc::elect_one()) {
+          const uint32_t lb = CTAS == 1 ? 0u : tc::address_in(&full[s], 0);
           // the leader's barrier counts the bytes of both CTAs
           if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * L::kStage);
           uint8_t *a = sA + (size_t)s * L::kA, *b = sB + (size_t)s * L::kB;
@@ -224,17 +191,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               load_box<CTAS>(b + i * 2 * kBox, &bmap, x, c0 + 128 * i, &full[s], lb);
           }
         }
-      }
-      if (*fail) {   // leave no copy in flight behind (the leader's barriers count both CTAs')
-        if (rank == 0) {
-          const uint32_t from = it > (uint32_t)S ? it - S : 0;
-          for (uint32_t i = from; i < it; ++i) mbar_wait(&full[i % S], (i / S) & 1u, tc::kWaitTries);
-        }
-        bad |= QAMW_STATUS_TIMEOUT;
+        __syncwarp();
       }
     }
+    if (*fail) {   // leave no copy in flight behind (the leader's barriers count both CTAs')
+      if (rank == 0) {
+        const uint32_t from = it > (uint32_t)S ? it - S : 0;
+        for (uint32_t i = from; i < it; ++i) mbar_wait(&full[i % S], (i / S) & 1u, tc::kWaitTries);
+      }
+      bad |= QAMW_STATUS_TIMEOUT;
+    }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // bf16 x bf16 -> fp32; bits 15, 16: operand rows contiguous
       constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) |
                                   ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(kBN >> 3) << 17) |
@@ -252,19 +220,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t s = it % S;
           if (!tc::wait(&full[s], (it / S) & 1u, fail)) { ok = false; break; }
           tc::fence_after();
-          const uint32_t a = smem_u32(sA + (size_t)s * L::kA), b = smem_u32(sB + (size_t)s * L::kB);
+          if (tc::elect_one()) {
+            const uint32_t a = smem_u32(sA + (size_t)s * L::kA), b = smem_u32(sB + (size_t)s * L::kB);
 #pragma unroll
-          for (int i = 0; i < kBK / 16; ++i)
-            mma_bf16<CTAS>(d, A_MN ? desc_mn_sw128(a + 2048 * i) : tc::desc_k_sw128(a + 32 * i),
-                           B_MN ? desc_mn_sw128(b + 2048 * i) : tc::desc_k_sw128(b + 32 * i), kIdesc,
-                           (k != w.k0 || i != 0) ? 1u : 0u);
-          commit<CTAS>(&empty[s]);
+            for (int i = 0; i < kBK / 16; ++i)
+              mma_bf16<CTAS>(d, A_MN ? desc_mn_sw128(a + 2048 * i) : tc::desc_k_sw128(a + 32 * i),
+                             B_MN ? desc_mn_sw128(b + 2048 * i) : tc::desc_k_sw128(b + 32 * i), kIdesc,
+                             (k != w.k0 || i != 0) ? 1u : 0u);
+            commit<CTAS>(&empty[s]);
+            if (k == w.k1 - 1) commit<CTAS>(&acc_full[buf]);
+          }
+          __syncwarp();
         }
-        if (ok) commit<CTAS>(&acc_full[buf]);
         ++seg;
       }
       if (*fail) {
-        commit<CTAS>(&drained);
+        if (tc::elect_one()) commit<CTAS>(&drained);
         mbar_wait(&drained, 0u, tc::kWaitTries);
         bad |= QAMW_STATUS_TIMEOUT;
       }
@@ -284,8 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const uint32_t buf = seg & 1u;
-      if (!tc::wait(&acc_full[buf], (seg >> 1) & 1u, fail)) { bad |= QAMW_STATUS_TIMEOUT; break; }
-      __syncwarp();
+      if (!tc::wait_warp(&acc_full[buf], (seg >> 1) & 1u, fail)) { bad |= QAMW_STATUS_TIMEOUT; break; }
       tc::fence_after();
       const int64_t row = w.rt * L::kRows + rank * 128 + 32 * wq + lane;
       const int64_t col0 = w.ct * kBN;
@@ -379,9 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         if constexpr (CTAS == 1) tc::mbar_arrive(&acc_empty[buf]);
-        else
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(&acc_empty[buf]))
-                       : "memory");
+        else tc::arrive_cluster(tc::address_in(&acc_empty[buf], 0));
       }
       ++seg;
     }
@@ -390,42 +358,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc::fence_before();
   __syncthreads();
-  if constexpr (CTAS == 2) cluster_sync();   // no CTA leaves while the pair's MMAs, copies or arrivals may reach it
+  if constexpr (CTAS == 2) tc::cluster_sync();   // no CTA leaves while the pair's MMAs, copies or arrivals may reach it
   if (warp == 1) {
     tc::fence_after();
     if constexpr (CTAS == 1) tc::dealloc(tmem, 512);
-    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    else tc::dealloc_pair(tmem, 512);
   }
   bad = __reduce_or_sync(0xffffffffu, bad);
   if (lane == 0) status_or(g.status, bad);
 }
 
-// loss and normaliser from the tiles' partial maxima and sums: 8 threads per
-// token take every eighth tile, then join in a fixed order.
-__global__ void __launch_bounds__(256) ce_finish_kernel(const float2 *partials, const float *target_logit,
-                                                        const int64_t *targets, int64_t T, int64_t V, int64_t n_tiles,
-                                                        int64_t ignore, float *loss, float *lse, int32_t *status) {
-  __shared__ float2 part[8][32];
+// loss and normaliser from the tiles' partial maxima and sums: 32 threads per
+// token take every 32nd tile, then join pairwise: a fixed order.
+constexpr int kFinishThreads = 1024;
+__global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const float2 *partials, const float *target_logit,
+                                                                   const int64_t *targets, int64_t T, int64_t V,
+                                                                   int64_t n_tiles, int64_t ignore, float *loss,
+                                                                   float *lse, int32_t *status) {
+  __shared__ float2 part[32][33];
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * 32 + lane;
-  float m = -INFINITY, s = 0.0f;
-  auto join = [&](float2 p) {
-    const float mn = fmaxf(m, p.x), ref = mn == -INFINITY ? 0.0f : mn;
-    s = s * exp2f(m - ref) + p.y * exp2f(p.x - ref);
-    m = mn;
+  auto join = [](float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.0f : m;
+    return make_float2(m, a.y * exp2f(a.x - ref) + b.y * exp2f(b.x - ref));
   };
-  if (t < T)
-    for (int64_t i = sl; i < n_tiles; i += 8) join(partials[i * T + t]);
-  part[sl][lane] = make_float2(m, s);
+  tc::griddep_wait();
+  float2 p = make_float2(-INFINITY, 0.0f);
+  if (t < T) {
+    for (int64_t i = sl; i < n_tiles; i += 128) {        // four loads in flight
+      float2 q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        q[k] = i + 32 * k < n_tiles ? partials[(i + 32 * k) * T + t] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p = join(p, q[k]);
+    }
+  }
+  part[sl][lane] = p;
   __syncthreads();
-  if (sl != 0 || t >= T) return;
-  for (int i = 1; i < 8; ++i) join(part[i][lane]);
-  const float n = __fmaf_rn(m, kLn2, logf(s));
-  const int64_t at = targets[t];
+  // warp w joins the 32 terms of token w: lane i holds term i
+  p = part[lane][sl];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+    p = join(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o), __shfl_xor_sync(0xffffffffu, p.y, o)));
+  const int64_t tt = (int64_t)blockIdx.x * 32 + sl;
+  if (lane != 0 || tt >= T) return;
+  const float n = __fmaf_rn(p.x, kLn2, logf(p.y));
+  const int64_t at = targets[tt];
   const bool real = at >= 0 && at < V;
   if (at != ignore && !real) status_or(status, QAMW_STATUS_BAD_INDEX);
-  lse[t] = n;
-  loss[t] = (at != ignore && real) ? n - target_logit[t] : 0.0f;
+  lse[tt] = n;
+  loss[tt] = (at != ignore && real) ? n - target_logit[tt] : 0.0f;
 }
 
 // X with the rows of ignored tokens set to zero, [T][K]: their G is zero, but
@@ -576,11 +559,18 @@ cudaError_t launch_ce_piece(const CeArgsIn &a, void *workspace, cudaStream_t s) 
 
 cudaError_t launch_ce_finish(const CeArgsIn &a, void *workspace, float *loss, float *lse, cudaStream_t s) {
   const CeWorkspace w = ce_workspace(a.T, a.V);
-  ce_finish_kernel<<<(unsigned)((a.T + 31) / 32), 256, 0, s>>>(
-      static_cast<const float2 *>(workspace),
-      reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.target_logit), a.targets, a.T, a.V,
-      vocab_tiles(a.V), a.ignore, loss, lse, a.status);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.T + 31) / 32), 1, 1);
+  cfg.blockDim = dim3(kFinishThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ce_finish_kernel, static_cast<const float2 *>(workspace),
+                            reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.target_logit),
+                            a.targets, a.T, a.V, vocab_tiles(a.V), a.ignore, loss, lse, a.status);
 }
 
 cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const float *grad, int64_t piece, bool first,

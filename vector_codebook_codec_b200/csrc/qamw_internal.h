@@ -215,6 +215,9 @@ struct Mx4MatmulArgs {
   qamw_dtype out_t;
   int64_t ldy;
   int32_t *status;
+  // the launch before this one in the stream is launch_mx4_quantize of x (and
+  // the weights are older): the kernel may start while x is being coded
+  int after_quantize = 0;
 };
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs &a, cudaStream_t s);
 

@@ -350,6 +350,13 @@ __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxReside
   // K % 32 == 0: a run of 16 columns and a group are all in or all out
   const bool in[2] = {at.run0 < p.K, at.run0 + 64 < p.K};
   const T *src = static_cast<const T *>(p.W) + at.run0;
+  // the product of mx4_linear may start: it waits for this kernel before it reads the codes
+  asm volatile("griddepcontrol.launch_dependents;");
+  uint32_t w0[N], w1[N];
+  if (rg < p.M) {
+    load16<T>(src + rg * p.ldw, p.vec, in[0], w0);
+    load16<T>(src + rg * p.ldw + 64, p.vec, in[1], w1);
+  }
   __shared__ Factors f;
   if (PREP)   // +-s, +-1/s or +-1; one far from 1 becomes NaN: its rows are decided from fp64
     form_factors(f, unit, p.K, [&](int64_t col) {
@@ -362,11 +369,6 @@ __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxReside
     });
   const float inv = (float)(1.0 / sqrt((double)(1 << LB)));
   uint32_t bad = 0;
-  uint32_t w0[N], w1[N];
-  if (rg < p.M) {
-    load16<T>(src + rg * p.ldw, p.vec, in[0], w0);
-    load16<T>(src + rg * p.ldw + 64, p.vec, in[1], w1);
-  }
   for (int64_t row = rg; row < rows_pad; row += p.row_groups) {
     uint32_t sword = 0;
     if (row < p.M) {

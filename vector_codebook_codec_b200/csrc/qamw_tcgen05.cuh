@@ -25,16 +25,47 @@ __device__ __forceinline__ void mbar_init_fence() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
-// Bounded wait: true once the phase has completed. It gives up, and raises the
-// CTA's failure flag, after kWaitTries attempts, and gives up early once
-// another role has raised it: every role then leaves its loop.
+// Loads and MMAs are issued by one lane of a warp whose 32 lanes walk the loop
+// together: the operands of these instructions are uniform registers, and only
+// in code that the compiler sees to be uniform are they formed without a
+// detour for every instruction (with the loop inside `if (lane == 0)` a stage
+// of the 4-bit kernels took 1.0 us, its MMAs 0.27).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+  return p != 0u;
+}
+
+// Bounded wait of a whole warp, one answer for all lanes: true once the phase
+// has completed. It gives up, and raises the CTA's failure flag, after
+// kWaitTries attempts, and gives up early once another role has raised it:
+// every role then leaves its loop.
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *fail) {
   for (uint32_t i = 0; i < kWaitTries; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 63u && *fail) return false;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 63u) == 63u && __any_sync(0xffffffffu, *fail != 0)) return false;
   }
   *fail = 1;
   return false;
+}
+
+// The same for a whole warp that waits long (an epilogue for its accumulators):
+// one lane asks, and sleeps between its attempts, so that the waiting takes
+// nothing from the warps that load and multiply.
+constexpr uint32_t kSleepTries = 1u << 21;   // attempts, at most 256 ns apart
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *fail) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) {
+    uint32_t ns = 32;
+    for (uint32_t i = 0; i < kSleepTries; ++i) {
+      if (mbar_try_wait(bar, parity)) { ok = 1; break; }
+      if (*fail) break;
+      __nanosleep(ns);
+      if (ns < 256) ns <<= 1;
+    }
+    if (!ok) *fail = 1;
+  }
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
 // Operand descriptor, 128-byte swizzle, K contiguous: rows of 128 bytes, 8-row
@@ -71,6 +102,72 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
                : "memory");
 }
 
+// ---- clusters and CTA pairs (cta_group::2) ----
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of this CTA's shared variable in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t address_in(const void *p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// A tile into this CTA's memory, counted at the barrier `bar` (a cluster
+// address) of either CTA of the pair.
+__device__ __forceinline__ void load_2d_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// to the barrier at this place in both CTAs of the pair
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void alloc_pair(uint32_t *slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc_pair(uint32_t tmem, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+}
+
+// ---- programmatic dependent launch ----
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+// The walk over n_r x n_c tiles: groups of `group` row tiles, the row varying
+// fastest inside a group, so that the row operand of a group stays in L2 while
+// the columns go by.
+struct TileWalk {
+  int64_t n_r, n_c, group;
+  __device__ __forceinline__ void at(int64_t t, int64_t &rt, int64_t &ct) const {
+    const int64_t per = group * n_c, g = t / per, in = t - g * per;
+    const int64_t left = n_r - g * group, h = left < group ? left : group;
+    ct = in / h;
+    rt = g * group + (in - ct * h);
+  }
+};
+
 // Tensor-memory allocation by one whole warp; `cols` a power of two >= 32.
 __device__ __forceinline__ void alloc(uint32_t *slot, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
@@ -81,6 +178,19 @@ __device__ __forceinline__ void dealloc(uint32_t tmem, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
 }
 
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 32 consecutive accumulator columns of the warp's 32 lanes, valid after ld_wait()
+__device__ __forceinline__ void ld32_async(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
 // 32 / 16 consecutive accumulator columns of the warp's 32 lanes
 __device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
