@@ -61,12 +61,14 @@ struct CeTile {
   static constexpr int kStage = kA + kB;
 };
 
-// Operand descriptor, 128-byte swizzle, rows (or columns) of the product
-// contiguous: a 64 x 64 box holds 64 contraction rows of 128 bytes; 8-row atoms
-// are 1024 bytes apart along the contraction, boxes 8192 bytes along the rows.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Operands whose rows (or columns) of the product are contiguous: a 64 x 64 box
+// holds 64 contraction rows of 128 bytes; 8-row atoms are 1024 bytes apart
+// along the contraction (as in the other layout), boxes 8192 bytes along the
+// rows (the leading offset). 16 contraction steps are 2048 bytes, or 32 bytes
+// where the contraction is contiguous.
+template <bool MN>
+__device__ __forceinline__ uint32_t operand_lo(const void *p) {
+  return tc::desc_lo(p, MN ? kBox >> 4 : 1);
 }
 
 template <int CTAS>
@@ -162,19 +164,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     uint32_t it = 0;
+    tc::Ring r;
     bool ok = true;
     for (int64_t u = first; u < n_units && ok; u += step) {
       const Unit w = unit_of(g, u);
       const int r0 = (int)(w.rt * L::kRows + rank * 128), c0 = (int)(w.ct * kBN + rank * L::kColsHere);
-      for (int64_t k = w.k0; k < w.k1; ++k, ++it) {
-        const uint32_t s = it % S;
-        if (!tc::wait(&empty[s], ((it / S) & 1u) ^ 1u, fail)) { ok = false; break; }
+      for (int k = (int)w.k0; k < (int)w.k1; ++k, ++it, r.next(S)) {
+        const uint32_t s = r.s;
+        if (!tc::wait(&empty[s], r.phase ^ 1u, fail)) { ok = false; break; }
         if (tc::elect_one()) {
           const uint32_t lb = CTAS == 1 ? 0u : tc::address_in(&full[s], 0);
           // the leader's barrier counts the bytes of both CTAs
           if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * L::kStage);
           uint8_t *a = sA + (size_t)s * L::kA, *b = sB + (size_t)s * L::kB;
-          const int x = (int)(k * kBK);
+          const int x = k * kBK;
           if constexpr (A_MN) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) load_box<CTAS>(a + i * kBox, &amap, r0 + 64 * i, x, &full[s], lb);
@@ -207,7 +210,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) |
                                   ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(kBN >> 3) << 17) |
                                   ((uint32_t)(L::kRows >> 4) << 24);
-      uint32_t it = 0, seg = 0;
+      const uint32_t a = operand_lo<A_MN>(sA), b = operand_lo<B_MN>(sB);
+      uint32_t seg = 0;
+      tc::Ring r;
       bool ok = true;
       for (int64_t u = first; u < n_units && ok; u += step) {
         const Unit w = unit_of(g, u);
@@ -216,19 +221,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!tc::wait(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u, fail)) break;
         tc::fence_after();
         const uint32_t d = tmem + buf * kBN;
-        for (int64_t k = w.k0; k < w.k1; ++k, ++it) {
-          const uint32_t s = it % S;
-          if (!tc::wait(&full[s], (it / S) & 1u, fail)) { ok = false; break; }
+        for (int k = (int)w.k0; k < (int)w.k1; ++k, r.next(S)) {
+          const uint32_t s = r.s;
+          if (!tc::wait(&full[s], r.phase, fail)) { ok = false; break; }
           tc::fence_after();
           if (tc::elect_one()) {
-            const uint32_t a = smem_u32(sA + (size_t)s * L::kA), b = smem_u32(sB + (size_t)s * L::kB);
+            const uint32_t sa = a + s * (L::kA >> 4), sb = b + s * (L::kB >> 4);
 #pragma unroll
             for (int i = 0; i < kBK / 16; ++i)
-              mma_bf16<CTAS>(d, A_MN ? desc_mn_sw128(a + 2048 * i) : tc::desc_k_sw128(a + 32 * i),
-                             B_MN ? desc_mn_sw128(b + 2048 * i) : tc::desc_k_sw128(b + 32 * i), kIdesc,
-                             (k != w.k0 || i != 0) ? 1u : 0u);
+              mma_bf16<CTAS>(d, tc::desc(sa + i * (A_MN ? 2048 >> 4 : 2), tc::kDescSw128Hi),
+                             tc::desc(sb + i * (B_MN ? 2048 >> 4 : 2), tc::kDescSw128Hi), kIdesc,
+                             (k != (int)w.k0 || i != 0) ? 1u : 0u);
             commit<CTAS>(&empty[s]);
-            if (k == w.k1 - 1) commit<CTAS>(&acc_full[buf]);
+            if (k == (int)w.k1 - 1) commit<CTAS>(&acc_full[buf]);
           }
           __syncwarp();
         }

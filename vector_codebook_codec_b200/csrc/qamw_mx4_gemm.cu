@@ -70,31 +70,27 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// A stage's scales into tensor memory: per 128 columns one scale tile of A and
-// XB of B.
-template <int CTAS, int XB>
-__device__ __forceinline__ void stage_scales(uint32_t fa, uint32_t fb, uint32_t sf, int left) {
-  const uint32_t sfa = sf, sfb = sf + 8;
+// One stage: its scales into tensor memory (per 128 columns one scale tile of A
+// and XB of B), then its MMAs of 64 columns; a scale tile's bytes 0-1 and 2-3
+// (the scale ids) serve two of them. FULL: 256 columns, without a test.
+// a, b, fa, fb: low descriptor words; sf: the stage's tensor-memory columns.
+template <int CTAS, int XB, bool FULL>
+__device__ __forceinline__ void stage(uint32_t d, uint32_t a, uint32_t b, uint32_t fa, uint32_t fb, uint32_t sf,
+                                      uint32_t idesc, int left, bool fresh) {
+  constexpr uint32_t kTile = kSfTile >> 4;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (left > 128 * h) {
-      cp_scales<CTAS>(sfa + 4 * h, tc::desc_scales(fa + kSfTile * h));
+    if (FULL || left > 128 * h) {
+      cp_scales<CTAS>(sf + 4 * h, tc::desc(fa + kTile * h, tc::kDescScalesHi));
 #pragma unroll
       for (int x = 0; x < XB; ++x)
-        cp_scales<CTAS>(sfb + 4 * (XB * h + x), tc::desc_scales(fb + 2 * kSfTile * x + kSfTile * h));
+        cp_scales<CTAS>(sf + 8 + 4 * (XB * h + x), tc::desc(fb + 2 * kTile * x + kTile * h, tc::kDescScalesHi));
     }
   }
-}
-// Its MMAs of 64 columns: a scale tile's bytes 0-1 and 2-3 (the scale ids)
-// serve two of them.
-template <int CTAS, int XB>
-__device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t a, uint32_t b, uint32_t sf, uint32_t idesc, int left,
-                                           bool fresh) {
-  const int n_mma = left >= kBK ? 4 : (left + 63) / 64;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (i < n_mma)
-      mma_mxf4<CTAS>(d, tc::desc_k_sw128(a + 32 * i), tc::desc_k_sw128(b + 32 * i),
+    if (FULL || left > 64 * i)
+      mma_mxf4<CTAS>(d, tc::desc(a + 2 * i, tc::kDescSw128Hi), tc::desc(b + 2 * i, tc::kDescSw128Hi),
                      idesc | ((uint32_t)(2 * (i & 1)) << 4) | ((uint32_t)(2 * (i & 1)) << 29), sf + 4 * (i >> 1),
                      sf + 8 + 4 * XB * (i >> 1), (!fresh || i != 0) ? 1u : 0u);
 }
@@ -151,8 +147,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 
   if (warp == 0) {
     auto sf_bytes = [&](int k) { return (uint32_t)(g.k_tiles - 2 * k >= 2 ? 2 * kSfTile : kSfTile); };
-    auto load_w = [&](int i) {
-      const int k = k0 + i, s = i % S;
+    auto load_w = [&](int k, uint32_t s) {
       if (tc::elect_one()) {
         mbar_arrive_expect_tx(&full[s], L::kA + L::kB + 2 * sf_bytes(k));
         tc::load_2d(sA + (size_t)s * L::kA, &wmap, k * kRowBytes, (int)(mt * 128), &full[s]);
@@ -160,8 +155,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
                       &full[s]);
       }
     };
-    auto load_x = [&](int i) {
-      const int k = k0 + i, s = i % S;
+    auto load_x = [&](int k, uint32_t s) {
       if (tc::elect_one()) {
         tc::load_2d(sB + (size_t)s * L::kB, &xmap, k * kRowBytes, 0, &full[s]);
         tc::load_bulk(sF + (size_t)s * 2 * L::kSf + L::kSf, g.x_scales + 2 * (int64_t)k * kSfTile, sf_bytes(k),
@@ -170,32 +164,34 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     };
     // the weights of the first stages are on their way while x is still being coded
     const int n = k1 - k0, early = min(n, S);
-    for (int i = 0; i < early; ++i) load_w(i);
+    for (int i = 0; i < early; ++i) load_w(k0 + i, i);
     if (g.after_quantize) tc::griddep_wait();
-    for (int i = 0; i < early; ++i) load_x(i);
+    for (int i = 0; i < early; ++i) load_x(k0 + i, i);
     int it = early;
-    for (; it < n; ++it) {
-      if (!tc::wait(&empty[it % S], ((it / S) & 1u) ^ 1u, fail)) break;
-      load_w(it);
-      load_x(it);
+    for (tc::Ring r; it < n; ++it, r.next(S)) {
+      if (!tc::wait(&empty[r.s], r.phase, fail)) break;
+      load_w(k0 + it, r.s);
+      load_x(k0 + it, r.s);
     }
     if (*fail) {   // leave no copy in flight behind
       for (int i = max(it - S, 0); i < it; ++i) mbar_wait(&full[i % S], (i / S) & 1u, tc::kWaitTries);
       bad |= QAMW_STATUS_TIMEOUT;
     }
   } else if (warp == 1) {
-    for (int k = k0; k < k1; ++k) {
-      const int it = k - k0, s = it % S;
-      if (!tc::wait(&full[s], (it / S) & 1u, fail)) { bad |= QAMW_STATUS_TIMEOUT; break; }
+    const uint32_t a = tc::desc_lo(sA), b = tc::desc_lo(sB), f = tc::desc_lo(sF);
+    tc::Ring r;
+    for (int k = k0; k < k1; ++k, r.next(S)) {
+      if (!tc::wait(&full[r.s], r.phase, fail)) { bad |= QAMW_STATUS_TIMEOUT; break; }
       tc::fence_after();
       if (tc::elect_one()) {
-        const uint32_t f = smem_u32(sF + (size_t)s * 2 * L::kSf);
-        const uint32_t sf = tmem + NT + (it % kSfBufs) * 16;
-        const int left = (int)(g.K - (int64_t)k * kBK);
-        stage_scales<1, 1>(f, f + L::kSf, sf, left);
-        stage_mmas<1, 1>(tmem, smem_u32(sA + (size_t)s * L::kA), smem_u32(sB + (size_t)s * L::kB), sf,
-                         idesc_of(128, NT), left, it == 0);
-        tc::commit(&empty[s]);
+        const uint32_t sa = a + r.s * (L::kA >> 4), sb = b + r.s * (L::kB >> 4), fs = f + r.s * (2 * L::kSf >> 4);
+        const uint32_t sf = tmem + NT + ((k - k0) % kSfBufs) * 16;
+        const int left = (int)g.K - k * kBK;
+        if (left >= kBK)
+          stage<1, 1, true>(tmem, sa, sb, fs, fs + (L::kSf >> 4), sf, idesc_of(128, NT), left, k == k0);
+        else
+          stage<1, 1, false>(tmem, sa, sb, fs, fs + (L::kSf >> 4), sf, idesc_of(128, NT), left, k == k0);
+        tc::commit(&empty[r.s]);
       }
       __syncwarp();
     }
@@ -315,7 +311,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0) {
     fail_flag = 0;
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 2);          // both CTAs announce their bytes at the leader's barrier
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&acc_full, 1);
@@ -336,24 +332,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     if (g.after_quantize) tc::griddep_wait();
     uint32_t it = 0;
+    tc::Ring r;
     bool ok = true;
     for (int64_t tile = first; tile < n_tiles && ok; tile += step) {
       int64_t rt, ct;
       g.walk.at(tile, rt, ct);
+      const int x0 = (int)(rt * 256 + rank * 128), w0 = (int)(ct * 256 + rank * 128);
       // first scale tiles of the rows; a tile past the last row is filled with zeros, and one past
       // the end of K (the next row's first) is not used
       const int xr = (int)((2 * rt + rank) * g.k_tiles), wr = (int)(2 * ct * g.k_tiles), kt = (int)g.k_tiles;
-      for (int k = 0; k < n_k; ++k, ++it) {
-        const uint32_t s = it % S;
-        if (!tc::wait(&empty[s], ((it / S) & 1u) ^ 1u, fail)) { ok = false; break; }
+      for (int k = 0; k < n_k; ++k, ++it, r.next(S)) {
+        if (!tc::wait(&empty[r.s], r.phase ^ 1u, fail)) { ok = false; break; }
         if (tc::elect_one()) {
-          const uint32_t lb = tc::address_in(&full[s], 0);
-          asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(lb),
-                       "r"(kPairStage)
-                       : "memory");
-          tc::load_2d_pair(sA + (size_t)s * kPairA, &xmap, k * kRowBytes, (int)(rt * 256 + rank * 128), lb);
-          tc::load_2d_pair(sB + (size_t)s * kPairB, &wmap, k * kRowBytes, (int)(ct * 256 + rank * 128), lb);
-          uint8_t *f = sF + (size_t)s * (kPairSfA + kPairSfB);
+          // the leader's barrier counts the bytes of both CTAs, and the leader alone announces them (an
+          // announcement of each CTA at the other's barrier cost more than the stage's MMAs)
+          if (rank == 0) mbar_arrive_expect_tx(&full[r.s], 2 * kPairStage);
+          const uint32_t lb = tc::address_in(&full[r.s], 0);
+          tc::load_2d_pair(sA + (size_t)r.s * kPairA, &xmap, k * kRowBytes, x0, lb);
+          tc::load_2d_pair(sB + (size_t)r.s * kPairB, &wmap, k * kRowBytes, w0, lb);
+          uint8_t *f = sF + (size_t)r.s * (kPairSfA + kPairSfB);
           tc::load_2d_pair(f, &xsmap, 0, xr + 2 * k, lb);
           tc::load_2d_pair(f + kPairSfA, &wsmap, 0, wr + 2 * k, lb);
           tc::load_2d_pair(f + kPairSfA + 2 * kSfTile, &wsmap, 0, wr + kt + 2 * k, lb);
@@ -370,23 +367,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      uint32_t it = 0, seg = 0;
+      const uint32_t a = tc::desc_lo(sA), b = tc::desc_lo(sB), f = tc::desc_lo(sF);
+      uint32_t sfb = 0, seg = 0;
+      tc::Ring r;
       bool ok = true;
       for (int64_t tile = first; tile < n_tiles && ok; tile += step, ++seg) {
         if (!tc::wait(&acc_empty, (seg & 1u) ^ 1u, fail)) break;
         tc::fence_after();
-        for (int k = 0; k < n_k; ++k, ++it) {
-          const uint32_t s = it % S;
-          if (!tc::wait(&full[s], (it / S) & 1u, fail)) { ok = false; break; }
+        for (int k = 0; k < n_k; ++k, r.next(S), sfb = (sfb + 1) % kSfBufs) {
+          if (!tc::wait(&full[r.s], r.phase, fail)) { ok = false; break; }
           tc::fence_after();
           if (tc::elect_one()) {
-            const uint32_t f = smem_u32(sF + (size_t)s * (kPairSfA + kPairSfB));
-            const uint32_t sf = tmem + 256 + (it % kSfBufs) * kPairSfCols;
-            const int left = (int)(g.K - (int64_t)k * kBK);
-            stage_scales<2, 2>(f, f + kPairSfA, sf, left);
-            stage_mmas<2, 2>(tmem, smem_u32(sA + (size_t)s * kPairA), smem_u32(sB + (size_t)s * kPairB), sf,
-                             idesc_of(256, 256), left, k == 0);
-            tc::commit_pair(&empty[s]);
+            const uint32_t sa = a + r.s * (kPairA >> 4), sb = b + r.s * (kPairB >> 4);
+            const uint32_t fs = f + r.s * ((kPairSfA + kPairSfB) >> 4), sf = tmem + 256 + sfb * kPairSfCols;
+            const int left = (int)g.K - k * kBK;
+            if (left >= kBK)
+              stage<2, 2, true>(tmem, sa, sb, fs, fs + (kPairSfA >> 4), sf, idesc_of(256, 256), left, k == 0);
+            else
+              stage<2, 2, false>(tmem, sa, sb, fs, fs + (kPairSfA >> 4), sf, idesc_of(256, 256), left, k == 0);
+            tc::commit_pair(&empty[r.s]);
             if (k == n_k - 1) tc::commit_pair(&acc_full);
           }
           __syncwarp();

@@ -68,18 +68,27 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// Operand descriptor, 128-byte swizzle, K contiguous: rows of 128 bytes, 8-row
-// atoms 1024 bytes apart (the leading offset is unused in this layout).
-__device__ __forceinline__ uint64_t desc_k_sw128(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// The place in a ring of `n` stages: index and phase, stepped without a
+// division (one costs a stage of the 4-bit kernels a tenth of its time).
+struct Ring {
+  uint32_t s = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++s == n) s = 0, phase ^= 1u;
+  }
+};
+
+// Operand descriptors: the low word holds the address / 16, so that stages and
+// steps inside a stage are additions to it.
+// 128-byte swizzle, K contiguous: rows of 128 bytes, 8-row atoms 1024 bytes
+// apart (the leading offset is unused in this layout).
+constexpr uint32_t kDescSw128Hi = (uint32_t)(1024 >> 4) | (1u << 14) | (2u << 29);
+// No swizzle, 16-byte rows, 8-row atoms of 128 contiguous bytes (scale tiles
+// for tcgen05.cp).
+constexpr uint32_t kDescScalesHi = (uint32_t)(128 >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_lo(const void *p, uint32_t leading = 1) {
+  return (smem_u32(p) >> 4) | (leading << 16);
 }
-// Scale factors for tcgen05.cp: no swizzle, 16-byte rows, 8-row atoms of 128
-// contiguous bytes.
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) |
-         ((uint64_t)1 << 46);
-}
+__device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
 
 // One TMA tile (x: innermost coordinate in elements, y: row) into shared memory.
 __device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
