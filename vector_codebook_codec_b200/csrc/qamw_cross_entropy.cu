@@ -314,22 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if constexpr (EPI == kGrad || EPI == kStore) {
-          if (in) {
-            __nv_bfloat16 *o = g.out + row * g.ldo + col0 + c;
-            if (n == 32 && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                __nv_bfloat162 h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-                reinterpret_cast<uint4 *>(o)[i] = *reinterpret_cast<const uint4 *>(h);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (j < n) o[j] = __float2bfloat16_rn(v[j]);
-            }
-          }
+          if (in) tc::store_row32(g.out + row * g.ldo + col0 + c, n, v);
         }
         if constexpr (EPI == kSlot) {
           if (in) {   // cols % 8 == 0: 16-byte groups are all in or all out

@@ -260,39 +260,6 @@ constexpr int kPairSfA = 2 * kSfTile, kPairSfB = 4 * kSfTile;       // but the s
 constexpr int kPairStage = kPairA + kPairB + kPairSfA + kPairSfB;
 constexpr int kPairSfCols = 24;                                     // tensor-memory columns of a stage's scales
 
-// 32 outputs of a token
-__device__ __forceinline__ void store_row32(const MxGemmArgs &g, int64_t t, int64_t m, const uint32_t *r) {
-  const int n = (int)(g.M - m < 32 ? g.M - m : 32);
-  if (g.out_bf16) {
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(g.Y) + t * g.ldy + m;
-    if (n == 32 && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          h[j] = __floats2bfloat162_rn(__uint_as_float(r[8 * i + 2 * j]), __uint_as_float(r[8 * i + 2 * j + 1]));
-        reinterpret_cast<uint4 *>(o)[i] = *reinterpret_cast<const uint4 *>(h);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) o[j] = __float2bfloat16_rn(__uint_as_float(r[j]));
-    }
-  } else {
-    float *o = static_cast<float *>(g.Y) + t * g.ldy + m;
-    if (n == 32 && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint4 *>(o)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) o[j] = __uint_as_float(r[j]);
-    }
-  }
-}
-
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx4_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                     const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
@@ -408,9 +375,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       g.walk.at(tile, rt, ct);
       if (!tc::wait_warp(&acc_full, seg & 1u, fail)) { bad |= QAMW_STATUS_TIMEOUT; break; }
       tc::fence_after();
-      uint32_t r[128];
+      float v[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc::ld32_async(tmem + 128 * half + 32 * c + ((uint32_t)(32 * wq) << 16), r + 32 * c);
+      for (int c = 0; c < 4; ++c) tc::ld32_async(tmem + 128 * half + 32 * c + ((uint32_t)(32 * wq) << 16), v + 32 * c);
       tc::ld_wait();
       tc::fence_before();
       __syncwarp();
@@ -418,8 +385,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int64_t t = rt * 256 + rank * 128 + 32 * wq + lane, m = ct * 256 + 128 * half;
       if (t < g.T) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (m + 32 * c < g.M) store_row32(g, t, m + 32 * c, r + 32 * c);
+        for (int c = 0; c < 4; ++c) {
+          const int64_t at = t * g.ldy + m + 32 * c, n = g.M - (m + 32 * c);
+          if (n > 0) {
+            if (g.out_bf16) tc::store_row32(static_cast<__nv_bfloat16 *>(g.Y) + at, n < 32 ? (int)n : 32, v + 32 * c);
+            else tc::store_row32(static_cast<float *>(g.Y) + at, n < 32 ? (int)n : 32, v + 32 * c);
+          }
+        }
       }
     }
   }

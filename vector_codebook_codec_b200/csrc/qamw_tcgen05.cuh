@@ -52,7 +52,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
 // The same for a whole warp that waits long (an epilogue for its accumulators):
 // one lane asks, and sleeps between its attempts, so that the waiting takes
 // nothing from the warps that load and multiply.
-constexpr uint32_t kSleepTries = 1u << 21;   // attempts, at most 256 ns apart
+constexpr uint32_t kSleepTries = 1u << 22;   // attempts, at most 128 ns apart
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *fail) {
   int ok = 0;
   if ((threadIdx.x & 31) == 0) {
@@ -61,7 +61,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
       if (mbar_try_wait(bar, parity)) { ok = 1; break; }
       if (*fail) break;
       __nanosleep(ns);
-      if (ns < 256) ns <<= 1;
+      if (ns < 128) ns <<= 1;
     }
     if (!ok) *fail = 1;
   }
@@ -177,6 +177,52 @@ struct TileWalk {
   }
 };
 
+// 32 contiguous outputs of a lane's row, `n` of them real: whole 32-byte sectors
+// where the address allows it (two 16-byte stores per sector double the
+// requests to L2), single values at a ragged end.
+__device__ __forceinline__ void store_32b(void *p, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store_row32(float *o, int n, const float *v) {
+  if (n >= 32 && reinterpret_cast<uintptr_t>(o) % 32 == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
+      store_32b(o + 8 * i, w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) o[j] = v[j];
+  }
+}
+__device__ __forceinline__ void store_row32(__nv_bfloat16 *o, int n, const float *v) {
+  if (n >= 32 && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    if (reinterpret_cast<uintptr_t>(o) % 32 == 0) {
+      store_32b(o, w);
+      store_32b(o + 16, w + 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) o[j] = __float2bfloat16_rn(v[j]);
+  }
+}
+
 // Tensor-memory allocation by one whole warp; `cols` a power of two >= 32.
 __device__ __forceinline__ void alloc(uint32_t *slot, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
@@ -189,14 +235,14 @@ __device__ __forceinline__ void dealloc(uint32_t tmem, uint32_t cols) {
 
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // 32 consecutive accumulator columns of the warp's 32 lanes, valid after ld_wait()
-__device__ __forceinline__ void ld32_async(uint32_t taddr, uint32_t *r) {
+__device__ __forceinline__ void ld32_async(uint32_t taddr, float *r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr)
       : "memory");
 }
