@@ -476,7 +476,7 @@ size_t qamw_mx4_linear_workspace_bytes(int64_t T, int64_t K);
  * Forward: qamw_cross_entropy_piece for every piece (in any order, one
  * stream), then qamw_cross_entropy_finish writes loss and lse (device float32
  * [T]). The workspace is qamw_cross_entropy_workspace_bytes(T, V) bytes: a
- * maximum and a sum per token and 256 entries, combined in a fixed order.
+ * maximum and a sum per token and 128 entries, combined in a fixed order.
  *
  * Backward: qamw_cross_entropy_grad_piece for every piece, one after another
  * (`first` != 0 for the first of them, `piece` the same in all calls and at

@@ -342,11 +342,11 @@ def test_mx4_scale_layout_rejects_bad_arguments(lib):
 
 
 def test_cross_entropy_workspace_bytes(lib):
-    """A maximum and a sum per token and 256 entries, then a logit per token."""
+    """A maximum and a sum per token and 128 entries, then a logit per token."""
     def a256(n):
         return (n + 255) // 256 * 256
     for T, V in ((1, 1), (300, 50021), (4096, 65536)):
-        assert lib.qamw_cross_entropy_workspace_bytes(T, V) == a256(8 * T * ((V + 255) // 256)) + a256(4 * T)
+        assert lib.qamw_cross_entropy_workspace_bytes(T, V) == a256(8 * T * ((V + 127) // 128)) + a256(4 * T)
     for T, V in ((0, 5), (5, 0), ((1 << 24) + 1, 5)):
         assert lib.qamw_cross_entropy_workspace_bytes(T, V) == 0
     assert lib.qamw_cross_entropy_grad_workspace_bytes(4, 8, 256) >= 4 * 256 * 2 + 4 * 8 * 6

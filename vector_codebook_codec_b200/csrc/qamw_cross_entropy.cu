@@ -4,6 +4,12 @@
 //   l_tv = sum_j X_tj W_vj;  lse_t = log sum_v exp l_tv;  loss_t = lse_t - l_t,target(t)
 //   G_tv = g_t (exp(l_tv - lse_t) - [v = target(t)]);  dX = G W;  dW = G^T X
 //
+// G is kept as G / max|g|, and the fp32 sums are multiplied by max|g|: with the
+// mean's equal g_t the entries near -1, which carry most of both gradients, are
+// then all but exact in bf16 instead of all being off by the rounding of g
+// (relative error of dX against 64 bits at 4096 tokens x 65536: 3.6e-3 -> the
+// 1.7e-3 of the output's own rounding).
+//
 // All three products run through one tcgen05 kernel (bf16 operands, fp32
 // accumulation in tensor memory) whose epilogue consumes the accumulators
 // where they are: the forward pass reduces a tile's 256 logits of a token to
@@ -26,7 +32,8 @@ namespace {
 
 constexpr int kBN = 256;          // columns per tile
 constexpr int kBK = 64;           // contraction per stage: 128 bytes of bf16
-constexpr int kThreads = 192;     // warp 0: loads, warp 1: MMA, warps 2-5: epilogue
+constexpr int kThreads = 320;     // warp 0: loads, warp 1: MMA, warps 2-9: epilogue
+constexpr int kHalf = 128;        // columns of a tile that an epilogue warp takes
 constexpr int kBox = 64 * 128;    // bytes of a 64 x 64 box
 constexpr int kMaxStages = 6;
 constexpr int kGroupRows = 16;    // row tiles walked together (their operand stays in L2)
@@ -43,9 +50,10 @@ struct CeArgs {
   // kStats, kGrad: rows are tokens, columns the vocabulary entries v0 ..
   const int64_t *targets;         // [T]
   int64_t v0, V, ignore;
-  float2 *partials;               // kStats: [tiles of the whole vocabulary][T] (max * log2 e, sum relative to it)
+  float2 *partials;               // kStats: [half tiles of the whole vocabulary][T] (max * log2 e, sum relative to it)
   float *target_logit;            // kStats: [T]
   const float *lse, *grad;        // kGrad: [T]
+  const float *factor;            // kGrad: of G (divided out); kStore: of D
   __nv_bfloat16 *out;             // kGrad: G, kStore: D
   int64_t ldo;
   float *slots;                   // kSlot: [splits][rows][cols] fp32
@@ -145,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4 * CTAS);
+      mbar_init(&acc_empty[i], 8 * CTAS);
     }
     mbar_init(&drained, 1);
     tc::mbar_init_fence();
@@ -246,28 +254,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    const int wq = warp & 3;
+    // a warp takes 32 rows x 128 columns, 32 columns at a time with the next 32 on their way
+    const int wq = warp & 3, half = (warp - 2) >> 2;
+    const float scale = EPI == kStore ? *g.factor : 1.0f;
     uint32_t seg = 0;
     for (int64_t u = first; u < n_units; u += step) {
       const Unit w = unit_of(g, u);
+      const int64_t row = w.rt * L::kRows + rank * 128 + 32 * wq + lane;
+      const int64_t col0 = w.ct * kBN + kHalf * half;
+      const int n_cols = (int)(g.cols - col0 < kHalf ? g.cols - col0 : kHalf);   // may be <= 0
+      const bool in = row < g.rows;
       if (w.k0 >= w.k1) {                  // a split without work: its slot is still a term of the sum
         if constexpr (EPI == kSlot) {
-          const int64_t r = w.rt * L::kRows + rank * 128 + 32 * wq + lane;
-          if (!g.add && r < g.rows)
-            for (int64_t c = w.ct * kBN; c < g.cols && c < (w.ct + 1) * kBN; ++c)
-              g.slots[((int64_t)w.split * g.rows + r) * g.cols + c] = 0.0f;
+          if (!g.add && in)
+            for (int c = 0; c < n_cols; ++c) g.slots[((int64_t)w.split * g.rows + row) * g.cols + col0 + c] = 0.0f;
         }
         continue;
       }
-      const uint32_t buf = seg & 1u;
-      if (!tc::wait_warp(&acc_full[buf], (seg >> 1) & 1u, fail)) { bad |= QAMW_STATUS_TIMEOUT; break; }
-      tc::fence_after();
-      const int64_t row = w.rt * L::kRows + rank * 128 + 32 * wq + lane;
-      const int64_t col0 = w.ct * kBN;
-      const int n_cols = (int)(g.cols - col0 < kBN ? g.cols - col0 : kBN);
-      const bool in = row < g.rows;
-      const uint32_t taddr = tmem + buf * kBN + ((uint32_t)(32 * wq) << 16);
-      int tcol = -1;                       // the target's column in this tile
+      int tcol = -1;                       // the target's column among this warp's
       float m = -INFINITY, sum = 0.0f;     // kStats
       float lse2 = 0.0f, gr = 0.0f;        // kGrad
       if constexpr (EPI == kStats || EPI == kGrad) {
@@ -277,18 +281,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live && off >= 0 && off < n_cols) tcol = (int)off;
         if constexpr (EPI == kGrad) {
           lse2 = in ? g.lse[row] * kLog2e : 0.0f;
-          gr = live ? g.grad[row] : 0.0f;
+          gr = live ? __fdiv_rn(g.grad[row], *g.factor) : 0.0f;
         }
       }
-      for (int c = 0; c < n_cols; c += 32) {
-        float v[32];
-        tc::ld32(taddr + (uint32_t)c, v);
+      const uint32_t buf = seg & 1u;
+      if (!tc::wait_warp(&acc_full[buf], (seg >> 1) & 1u, fail)) { bad |= QAMW_STATUS_TIMEOUT; break; }
+      tc::fence_after();
+      const uint32_t taddr = tmem + buf * kBN + kHalf * half + ((uint32_t)(32 * wq) << 16);
+      float buffer[2][32];
+      if (n_cols > 0) tc::ld32_async(taddr, buffer[0]);
+#pragma unroll
+      for (int q = 0; q < kHalf / 32; ++q) {
+        const int c = 32 * q;
+        if (c >= n_cols) break;
+        float(&v)[32] = buffer[q & 1];
+        tc::ld_wait();
+        tc::tie32(v);
+        if (c + 32 < n_cols) tc::ld32_async(taddr + (uint32_t)c + 32, buffer[(q + 1) & 1]);
         const int n = n_cols - c < 32 ? n_cols - c : 32;
         if constexpr (EPI == kStats) {
           if (tcol >= c && tcol < c + 32) {
+            // a sum with one term: a choice among registers would be made through memory
             float z = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) z = (j == tcol - c) ? v[j] : z;
+            for (int j = 0; j < 32; ++j) z = __fadd_rn(z, j == tcol - c ? v[j] : 0.0f);
             g.target_logit[row] = z;
           }
           if (n < 32) {
@@ -313,28 +329,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[j] = none ? 0.0f : gr * p;
           }
         }
+        if constexpr (EPI == kStore) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= scale;
+        }
         if constexpr (EPI == kGrad || EPI == kStore) {
           if (in) tc::store_row32(g.out + row * g.ldo + col0 + c, n, v);
         }
         if constexpr (EPI == kSlot) {
           if (in) {   // cols % 8 == 0: 16-byte groups are all in or all out
             float4 *o = reinterpret_cast<float4 *>(g.slots + ((int64_t)w.split * g.rows + row) * g.cols + col0 + c);
+            if (g.add) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (4 * i < n) {
-                float4 q = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                if (g.add) {
+              for (int i = 0; i < 8; ++i) {
+                if (4 * i < n) {
                   const float4 p = o[i];
-                  q.x += p.x, q.y += p.y, q.z += p.z, q.w += p.w;
+                  v[4 * i] += p.x, v[4 * i + 1] += p.y, v[4 * i + 2] += p.z, v[4 * i + 3] += p.w;
                 }
-                o[i] = q;
               }
             }
+            tc::store_row32(reinterpret_cast<float *>(o), n, v);
           }
         }
       }
       if constexpr (EPI == kStats)
-        if (in) g.partials[((g.v0 + col0) / kBN) * g.rows + row] = make_float2(m, sum);
+        if (in && n_cols > 0) g.partials[((g.v0 + col0) / kHalf) * g.rows + row] = make_float2(m, sum);
       tc::fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -401,34 +420,58 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const float2 
   loss[tt] = (at != ignore && real) ? n - target_logit[tt] : 0.0f;
 }
 
-// X with the rows of ignored tokens set to zero, [T][K]: their G is zero, but
-// dW = G^T X would still turn an Inf or NaN of a padded row into NaN. Eight
-// columns a thread.
-__global__ void __launch_bounds__(256) ce_live_rows_kernel(const uint4 *X, int64_t ldx8, const int64_t *targets,
-                                                           int64_t T, int64_t K8, int64_t V, int64_t ignore,
-                                                           uint4 *out) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * K8; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / K8, c = i - t * K8, at = targets[t];
-    out[i] = (at != ignore && at >= 0 && at < V) ? X[t * ldx8 + c] : make_uint4(0u, 0u, 0u, 0u);
+// Before the backward pass. CTA 0: the factor of G, max |g| over the tokens that
+// count (1 if that is 0, Inf or NaN). The others: X with the rows of ignored
+// tokens set to zero, [T][K], eight columns a thread: their G is zero, but dW =
+// G^T X would still turn an Inf or NaN of a padded row into NaN.
+__global__ void __launch_bounds__(256) ce_prepare_kernel(const uint4 *X, int64_t ldx8, const int64_t *targets,
+                                                         const float *grad, int64_t T, int64_t K8, int64_t V,
+                                                         int64_t ignore, uint4 *live, float *factor) {
+  auto counts = [&](int64_t t) {
+    const int64_t at = targets[t];
+    return at != ignore && at >= 0 && at < V;
+  };
+  if (blockIdx.x == 0) {
+    __shared__ uint32_t part[8];
+    uint32_t top = 0;   // magnitudes as integers: ordered alike, NaN the largest
+    for (int64_t t = threadIdx.x; t < T; t += 256)
+      if (counts(t)) top = max(top, __float_as_uint(grad[t]) & 0x7FFFFFFFu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 8; ++i) top = max(top, part[i]);
+      *factor = top == 0u || top >= 0x7F800000u ? 1.0f : __uint_as_float(top);
+    }
+    return;
+  }
+  for (int64_t i = (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x; i < T * K8; i += (int64_t)(gridDim.x - 1) * 256) {
+    const int64_t t = i / K8;
+    live[i] = counts(t) ? X[t * ldx8 + (i - t * K8)] : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
-// dX = the sum of the slots, in order, rounded to bf16 (four values a thread)
-__global__ void __launch_bounds__(256) ce_sum_slots_kernel(const float *slots, int splits, int64_t T, int64_t K,
-                                                           __nv_bfloat16 *dX, int64_t ldx) {
+// dX = the sum of the slots, in order, times the factor of G, rounded to bf16
+// (four columns a thread)
+__global__ void __launch_bounds__(256) ce_sum_slots_kernel(const float *slots, int splits, const float *factor,
+                                                           int64_t T, int64_t K, __nv_bfloat16 *dX, int64_t ldx) {
   const int64_t n = T * K / 4;
+  const float f = *factor;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     float4 a = reinterpret_cast<const float4 *>(slots)[i];
     for (int s = 1; s < splits; ++s) {
       const float4 b = reinterpret_cast<const float4 *>(slots + (int64_t)s * T * K)[i];
       a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
     }
-    const int64_t row = 4 * i / K, col = 4 * i % K;
+    const int64_t row = 4 * i / K, col = 4 * i - row * K;
     __nv_bfloat16 *o = dX + row * ldx + col;
-    o[0] = __float2bfloat16_rn(a.x);
-    o[1] = __float2bfloat16_rn(a.y);
-    o[2] = __float2bfloat16_rn(a.z);
-    o[3] = __float2bfloat16_rn(a.w);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a.x * f, a.y * f), q = __floats2bfloat162_rn(a.z * f, a.w * f);
+    if (reinterpret_cast<uintptr_t>(o) % 8 == 0) {
+      *reinterpret_cast<uint2 *>(o) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&q));
+    } else {
+      o[0] = p.x, o[1] = p.y, o[2] = q.x, o[3] = q.y;
+    }
   }
 }
 
@@ -482,30 +525,41 @@ cudaError_t run(const Operand &A, const Operand &B, CeArgs g, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, amap, bmap, g);
 }
 
-// one CTA per tile when 128 rows hold everything, else a pair
+// One CTA per tile, or a pair. A step of either takes the same time, so the
+// fewer waves win; the pair does on a tie, since it loads a third less (4096
+// tokens x 32000 x 4096: 670 us in pairs, 830 in single CTAs; gradient of 301
+// tokens x 50021 x 2048: 256 in pairs, 236 by this rule). A contraction of at
+// most 8 steps is bound by its epilogue, which single CTAs overlap better (the
+// same gradient with dW in single CTAs: 225; of 768 tokens, 12 steps: 235 in
+// pairs, 243).
+bool single_cta(int64_t rows, int64_t depth, int64_t tiles_c) {
+  if (depth <= 8 * kBK) return true;
+  const int64_t one = ((rows + 127) / 128) * tiles_c, pair = ((rows + 255) / 256) * tiles_c;
+  const int64_t sms = sm_count();
+  return (one + sms - 1) / sms < (pair + sms / 2 - 1) / (sms / 2);
+}
 template <bool A_MN, bool B_MN, int EPI>
 cudaError_t run_rows(const Operand &A, const Operand &B, const CeArgs &g, cudaStream_t s) {
-  return g.rows <= 128 ? run<1, A_MN, B_MN, EPI>(A, B, g, s) : run<2, A_MN, B_MN, EPI>(A, B, g, s);
+  const int64_t tiles_c = (g.cols + kBN - 1) / kBN * g.splits;
+  return single_cta(g.rows, g.depth, tiles_c) ? run<1, A_MN, B_MN, EPI>(A, B, g, s)
+                                              : run<2, A_MN, B_MN, EPI>(A, B, g, s);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-int64_t vocab_tiles(int64_t V) { return (V + kBN - 1) / kBN; }
+int64_t vocab_tiles(int64_t V) { return (V + kHalf - 1) / kHalf; }   // that have a partial maximum and sum
 
-// Contraction splits of dX for pieces of `piece` vocabulary entries: the
-// smallest number that fills the machine's waves to 90% (or the fullest up to
-// 32), each split at least 8 steps long.
+// Contraction splits of dX for pieces of `piece` vocabulary entries: the number
+// up to 32, each split at least 8 steps long, with the least waves x (steps + 4).
 int dx_splits(int64_t T, int64_t K, int64_t piece) {
-  const int ctas = T <= 128 ? 1 : 2;
-  const int64_t tiles = ((T + 128 * ctas - 1) / (128 * ctas)) * ((K + kBN - 1) / kBN);
-  const int64_t slots = sm_count() / ctas, steps = (piece + kBK - 1) / kBK;
+  const int64_t tiles_c = (K + kBN - 1) / kBN, steps = (piece + kBK - 1) / kBK, sms = sm_count();
   int best = 1;
-  double best_fill = 0.0;
+  int64_t least = INT64_MAX;
   for (int s = 1; s <= 32 && (s == 1 || steps / s >= 8); ++s) {
-    const int64_t units = tiles * s, waves = (units + slots - 1) / slots;
-    const double fill = (double)units / (double)(waves * slots);
-    if (fill > best_fill) best = s, best_fill = fill;
-    if (fill >= 0.9) break;
+    const int ctas = single_cta(T, piece, tiles_c * s) ? 1 : 2;
+    const int64_t units = ((T + 128 * ctas - 1) / (128 * ctas)) * tiles_c * s;
+    const int64_t cost = (units + sms / ctas - 1) / (sms / ctas) * ((steps + s - 1) / s + 4);
+    if (cost < least) best = s, least = cost;
   }
   return best;
 }
@@ -523,7 +577,8 @@ CeGradWorkspace ce_grad_workspace(int64_t T, int64_t K, int64_t piece) {
   CeGradWorkspace w;
   w.ldg = (piece + 7) / 8 * 8;
   w.live = align256((size_t)T * (size_t)w.ldg * 2);
-  w.slots = w.live + align256((size_t)T * (size_t)K * 2);
+  w.factor = w.live + align256((size_t)T * (size_t)K * 2);
+  w.slots = w.factor + 256;
   w.splits = dx_splits(T, K, piece);
   w.total = w.slots + align256((size_t)w.splits * (size_t)T * (size_t)K * 4);
   return w;
@@ -568,10 +623,11 @@ cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const floa
   const CeGradWorkspace w = ce_grad_workspace(a.T, a.K, piece);
   __nv_bfloat16 *G = static_cast<__nv_bfloat16 *>(workspace);
   uint4 *live = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(workspace) + w.live);
+  float *factor = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + w.factor);
   if (first) {
     const int64_t blocks = (a.T * a.K / 8 + 255) / 256, most = (int64_t)sm_count() * 16;
-    ce_live_rows_kernel<<<(unsigned)std::min(blocks, most), 256, 0, s>>>(
-        static_cast<const uint4 *>(a.X), a.ldx / 8, a.targets, a.T, a.K / 8, a.V, a.ignore, live);
+    ce_prepare_kernel<<<(unsigned)(1 + std::min(blocks, most)), 256, 0, s>>>(
+        static_cast<const uint4 *>(a.X), a.ldx / 8, a.targets, grad, a.T, a.K / 8, a.V, a.ignore, live, factor);
     const cudaError_t c = cudaGetLastError();
     if (c != cudaSuccess) return c;
   }
@@ -589,6 +645,7 @@ cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const floa
   g.ignore = a.ignore;
   g.lse = lse;
   g.grad = grad;
+  g.factor = factor;
   g.out = G;
   g.ldo = w.ldg;
   cudaError_t e = run_rows<false, false, kGrad>(X, {a.W, a.n, a.K, a.ldw}, g, s);
@@ -611,6 +668,7 @@ cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const floa
   d.splits = 1;
   d.steps_per_split = (a.T + kBK - 1) / kBK;
   d.status = a.status;
+  d.factor = factor;
   d.out = static_cast<__nv_bfloat16 *>(dW);
   d.ldo = lddw;
   return run_rows<true, true, kStore>({G, a.T, a.n, w.ldg}, X, d, s);
@@ -621,8 +679,8 @@ cudaError_t launch_ce_grad_finish(int64_t T, int64_t K, int64_t piece, void *dX,
   const CeGradWorkspace w = ce_grad_workspace(T, K, piece);
   const int64_t blocks = (T * K / 4 + 255) / 256, most = (int64_t)sm_count() * 16;
   ce_sum_slots_kernel<<<(unsigned)std::min(blocks, most), 256, 0, s>>>(
-      reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.slots), w.splits, T, K,
-      static_cast<__nv_bfloat16 *>(dX), lddx);
+      reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.slots), w.splits,
+      reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.factor), T, K, static_cast<__nv_bfloat16 *>(dX), lddx);
   return cudaGetLastError();
 }
 

@@ -239,9 +239,9 @@ struct CeWorkspace {       // tile maxima and sums, then the targets' logits [T]
 CeWorkspace ce_workspace(int64_t T, int64_t V);
 cudaError_t launch_ce_piece(const CeArgsIn &a, void *workspace, cudaStream_t s);
 cudaError_t launch_ce_finish(const CeArgsIn &a, void *workspace, float *loss, float *lse, cudaStream_t s);
-struct CeGradWorkspace {   // G bf16 [T][ldg], X without its ignored rows bf16 [T][K], the fp32 slots of dX [splits][T][K]
-  int64_t ldg;
-  size_t live, slots, total;
+struct CeGradWorkspace {   // G / factor bf16 [T][ldg], X without its ignored rows bf16 [T][K], the factor, the fp32
+  int64_t ldg;             // slots of dX [splits][T][K]
+  size_t live, factor, slots, total;
   int splits;
 };
 CeGradWorkspace ce_grad_workspace(int64_t T, int64_t K, int64_t piece);

@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tc::ld32_async(tmem + 128 * half + 32 * c + ((uint32_t)(32 * wq) << 16), v + 32 * c);
       tc::ld_wait();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::tie32(v + 32 * c);
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::arrive_cluster(tc::address_in(&acc_empty, 0));
