@@ -301,10 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = n_cols - c < 32 ? n_cols - c : 32;
         if constexpr (EPI == kStats) {
           if (tcol >= c && tcol < c + 32) {
-            // a sum with one term: a choice among registers would be made through memory
-            float z = 0.0f;
+            float z = 0.0f;   // moved under a predicate: a choice in C++ is made through local memory
 #pragma unroll
-            for (int j = 0; j < 32; ++j) z = __fadd_rn(z, j == tcol - c ? v[j] : 0.0f);
+            for (int j = 0; j < 32; ++j)
+              asm volatile("{ .reg .pred p; setp.eq.s32 p, %2, %3; @p mov.f32 %0, %1; }" : "+f"(z) : "f"(v[j]), "r"(tcol - c), "r"(j));
             g.target_logit[row] = z;
           }
           if (n < 32) {
