@@ -555,6 +555,11 @@ def _raw_stream(device):
     return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
+def _run(name, rc):
+    if rc != QAMW_OK:
+        _check(name, rc)
+
+
 def _address(t):
     return None if t is None else t.data_ptr()
 
@@ -586,11 +591,12 @@ def _need_status(device, status):
 
 
 def _need_scale(device, col_scale, K):
-    if col_scale is not None:
-        _need_cuda("col_scale", col_scale, _torch().float32, 1)
+    torch = _torch()
+    if col_scale is not None and not (col_scale.dtype == torch.float32 and col_scale.shape == (K,)
+                                      and col_scale.device == device and (K == 1 or col_scale.stride(0) == 1)):
+        _need_cuda("col_scale", col_scale, torch.float32, 1)
         _same_device(device, col_scale=col_scale)
-        if col_scale.shape[0] != K or (K > 1 and col_scale.stride(0) != 1):
-            raise ValueError("col_scale must be K contiguous values")
+        raise ValueError("col_scale must be K contiguous values")
 
 
 def mx4_scale_bytes(M: int, K: int) -> int:
@@ -600,21 +606,25 @@ def mx4_scale_bytes(M: int, K: int) -> int:
 
 
 def _need_mx4(name, q):
-    """The tensors of an Mx4 agree with its shape (the kernels trust them)."""
+    """The tensors of an Mx4 agree with its shape (the kernels trust them);
+    returns their device. One test for the good case, then what is wrong."""
     torch = _torch()
     if not isinstance(q, Mx4):
         raise ValueError(f"{name} must be an Mx4")
-    codes, scales = q.codes, q.scales
-    _need_cuda(f"{name}.codes", codes, torch.uint8, 2)
-    _need_cuda(f"{name}.scales", scales, torch.uint8, 1)
-    if codes.shape != (q.M, q.K // 2) or not codes.is_contiguous():
-        raise ValueError(f"{name}.codes must be contiguous [M, K/2]")
-    if scales.numel() != mx4_scale_bytes(q.M, q.K) or not scales.is_contiguous():
-        raise ValueError(f"{name}.scales must be qamw_mx4_scale_bytes(M, K) contiguous bytes")
-    device = codes.device
-    if scales.device != device:
+    codes, scales, s, K = q.codes, q.scales, q.col_scale, q.K
+    device, n = codes.device, mx4_scale_bytes(q.M, K)
+    if not (codes.is_cuda and codes.dtype == torch.uint8 and codes.shape == (q.M, K // 2) and codes.is_contiguous()
+            and scales.dtype == torch.uint8 and scales.shape == (n,) and scales.is_contiguous()
+            and scales.device == device):
+        _need_cuda(f"{name}.codes", codes, torch.uint8, 2)
+        _need_cuda(f"{name}.scales", scales, torch.uint8, 1)
+        if codes.shape != (q.M, K // 2) or not codes.is_contiguous():
+            raise ValueError(f"{name}.codes must be contiguous [M, K/2]")
+        if scales.numel() != n or not scales.is_contiguous():
+            raise ValueError(f"{name}.scales must be qamw_mx4_scale_bytes(M, K) contiguous bytes")
         raise ValueError(f"{name}.scales must be on {device}, got {scales.device}")
-    _need_scale(device, q.col_scale, q.K)
+    if s is not None:
+        _need_scale(device, s, K)
     return device
 
 
@@ -749,24 +759,22 @@ def mx4_linear(W: Mx4, X, out_dtype=None, status=None, stream=None, out=None):
     device = _need_mx4("W", W)
     if W.divide:
         raise ValueError("W was quantised with divide=True: it is the activations' side of a product")
-    _need_cuda("X", X, ndim=2)
     if X.device != device:
         raise ValueError(f"X must be on {device}, got {X.device}")
-    xt, ldx = _wdtype(X), _ld(X)
-    T, K = X.shape
-    if K != W.K:
-        raise ValueError("X must have K columns")
-    _need_status(device, status)
-    lib = load_library()
+    if X.dim() != 2 or X.shape[1] != W.K:
+        raise ValueError("X must be 2-D with K columns")
+    xt, ldx, T, K, M = _wdtype(X), _ld(X), X.shape[0], W.K, W.M
+    if status is not None:
+        _need_status(device, status)
     nws = ((T * (K // 2) + 255) & ~255) + mx4_scale_bytes(T, K)    # qamw_mx4_linear_workspace_bytes(T, K)
     with _on(device, stream):
         ws = torch.empty(nws, dtype=torch.uint8, device=device)
         if out is None:
-            out, ld = torch.empty((T, W.M), dtype=out_dtype, device=device), W.M
+            out, ld = torch.empty((T, M), dtype=out_dtype, device=device), M
         else:
-            ld = _need_out("out", out, (T, W.M), out_dtype, device)
-        _check("qamw_mx4_linear", lib.qamw_mx4_linear(
-            W.codes.data_ptr(), W.scales.data_ptr(), W.M, X.data_ptr(), xt, T, K, ldx, _address(W.col_scale), W.block,
+            ld = _need_out("out", out, (T, M), out_dtype, device)
+        _run("qamw_mx4_linear", load_library().qamw_mx4_linear(
+            W.codes.data_ptr(), W.scales.data_ptr(), M, X.data_ptr(), xt, T, K, ldx, _address(W.col_scale), W.block,
             W.seed & (2**64 - 1), out.data_ptr(), ot, ld, ws.data_ptr(), nws, _address(status), _raw_stream(device)))
     return out
 
