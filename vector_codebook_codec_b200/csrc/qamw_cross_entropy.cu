@@ -35,7 +35,7 @@ constexpr int kBK = 64;           // contraction per stage: 128 bytes of bf16
 constexpr int kThreads = 320;     // warp 0: loads, warp 1: MMA, warps 2-9: epilogue
 constexpr int kHalf = 128;        // columns of a tile that an epilogue warp takes
 constexpr int kBox = 64 * 128;    // bytes of a 64 x 64 box
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 8;
 constexpr int kGroupRows = 16;    // row tiles walked together (their operand stays in L2)
 
 enum Epilogue { kStats = 0, kGrad = 1, kStore = 2, kSlot = 3 };
@@ -46,6 +46,7 @@ struct CeArgs {
   int splits;                     // contraction split (kSlot only)
   int64_t steps_per_split;
   int stages;
+  int a_bytes;                    // of a stage's row operand: rows x 128
   int32_t *status;
   // kStats, kGrad: rows are tokens, columns the vocabulary entries v0 ..
   const int64_t *targets;         // [T]
@@ -64,9 +65,8 @@ template <int CTAS>
 struct CeTile {
   static constexpr int kRows = 128 * CTAS;                  // rows per tile
   static constexpr int kColsHere = kBN / CTAS;              // operand columns that one CTA loads
-  static constexpr int kA = 128 * 128;                      // bytes per stage
+  static constexpr int kA = 128 * 128;                      // bytes per stage, at most (CeArgs::a_bytes)
   static constexpr int kB = kColsHere * 128;
-  static constexpr int kStage = kA + kB;
 };
 
 // Operands whose rows (or columns) of the product are contiguous: a 64 x 64 box
@@ -133,7 +133,7 @@ template <int CTAS, bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, CeArgs g) {
   using L = CeTile<CTAS>;
-  if constexpr (EPI == kStats) tc::griddep_launch_dependents();   // ce_finish_kernel, which waits for this one
+  tc::griddep_launch_dependents();   // the next kernel may set up; it waits for this one before it reads or writes
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_slot;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 1 ? 0u : tc::cta_rank();
   const int S = g.stages;
-  uint8_t *sA = smem, *sB = smem + (size_t)S * L::kA;
+  uint8_t *sA = smem, *sB = smem + S * g.a_bytes;
 
   if (threadIdx.x == 0) {
     fail_flag = 0;
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if constexpr (CTAS == 2) tc::cluster_sync();   // both CTAs' barriers exist before either is signalled
   tc::fence_after();
+  tc::griddep_wait();
   const uint32_t tmem = tmem_slot;
   const int64_t n_units = g.n_r * g.n_c * g.splits, step = gridDim.x / CTAS, first = blockIdx.x / CTAS;
   uint32_t bad = 0;
@@ -183,8 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tc::elect_one()) {
           const uint32_t lb = CTAS == 1 ? 0u : tc::address_in(&full[s], 0);
           // the leader's barrier counts the bytes of both CTAs
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * L::kStage);
-          uint8_t *a = sA + (size_t)s * L::kA, *b = sB + (size_t)s * L::kB;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * (g.a_bytes + L::kB));
+          uint8_t *a = sA + s * g.a_bytes, *b = sB + (size_t)s * L::kB;
           const int x = k * kBK;
           if constexpr (A_MN) {
 #pragma unroll
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!tc::wait(&full[s], r.phase, fail)) { ok = false; break; }
           tc::fence_after();
           if (tc::elect_one()) {
-            const uint32_t sa = a + s * (L::kA >> 4), sb = b + s * (L::kB >> 4);
+            const uint32_t sa = a + s * ((uint32_t)g.a_bytes >> 4), sb = b + s * (L::kB >> 4);
 #pragma unroll
             for (int i = 0; i < kBK / 16; ++i)
               mma_bf16<CTAS>(d, tc::desc(sa + i * (A_MN ? 2048 >> 4 : 2), tc::kDescSw128Hi),
@@ -391,6 +392,7 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const float2 
     const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.0f : m;
     return make_float2(m, a.y * exp2f(a.x - ref) + b.y * exp2f(b.x - ref));
   };
+  tc::griddep_launch_dependents();
   tc::griddep_wait();
   float2 p = make_float2(-INFINITY, 0.0f);
   if (t < T) {
@@ -427,6 +429,7 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const float2 
 __global__ void __launch_bounds__(256) ce_prepare_kernel(const uint4 *X, int64_t ldx8, const int64_t *targets,
                                                          const float *grad, int64_t T, int64_t K8, int64_t V,
                                                          int64_t ignore, uint4 *live, float *factor) {
+  tc::griddep_launch_dependents();
   auto counts = [&](int64_t t) {
     const int64_t at = targets[t];
     return at != ignore && at >= 0 && at < V;
@@ -496,8 +499,14 @@ struct Operand {
 template <int CTAS, bool A_MN, bool B_MN, int EPI>
 cudaError_t run(const Operand &A, const Operand &B, CeArgs g, cudaStream_t s) {
   using L = CeTile<CTAS>;
+  // At most 120 rows: only they (in eights) are loaded, which leaves room for
+  // more stages; the MMA reads what follows them in shared memory as rows whose
+  // results no one looks at. (16 tokens x 32000 x 2048: filling the other 112
+  // rows with zeros took 5 of 38 us.)
+  const int a_rows = A_MN || CTAS == 2 ? 128 : (int)std::min<int64_t>(128, (g.rows + 7) / 8 * 8);
+  g.a_bytes = a_rows * 128;
   CUtensorMap amap, bmap;
-  if (!make_map(&amap, A.p, A.rows, A.cols, A.ld, A_MN ? 64 : 128, 64) ||
+  if (!make_map(&amap, A.p, A.rows, A.cols, A.ld, A_MN ? 64 : a_rows, 64) ||
       !make_map(&bmap, B.p, B.rows, B.cols, B.ld, B_MN ? 64 : 128, 64))
     return cudaErrorInvalidValue;
   int dev = 0, smem_max = 0;
@@ -506,8 +515,8 @@ cudaError_t run(const Operand &A, const Operand &B, CeArgs g, cudaStream_t s) {
   if ((e = cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
   g.n_r = (g.rows + L::kRows - 1) / L::kRows;
   g.n_c = (g.cols + kBN - 1) / kBN;
-  g.stages = (int)std::min<int64_t>(kMaxStages, (smem_max - 2048) / L::kStage);
-  const size_t smem = 1024 + (size_t)g.stages * L::kStage;
+  g.stages = (int)std::min<int64_t>(kMaxStages, (smem_max - 2048) / (g.a_bytes + L::kB));
+  const size_t smem = 1024 + (size_t)g.stages * (g.a_bytes + L::kB);
   auto kern = ce_gemm_kernel<CTAS, A_MN, B_MN, EPI>;
   if ((e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -515,13 +524,15 @@ cudaError_t run(const Operand &A, const Operand &B, CeArgs g, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CTAS;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set up beside the kernel before this one
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, amap, bmap, g);
 }
 

@@ -318,7 +318,9 @@ __device__ __forceinline__ float2 factor(const Factors &f, int lane, int j) {
 }
 template <typename F>
 __device__ __forceinline__ void form_factors(Factors &f, int64_t unit, int64_t K, F of) {
-  for (int i = threadIdx.x; i < kMxUnit; i += blockDim.x) {
+#pragma unroll
+  for (int n = 0; n < kMxUnit / (32 * kMxWarps); ++n) {   // a fixed count: the loads of s go out together
+    const int i = threadIdx.x + n * 32 * kMxWarps;
     const int64_t col = unit * kMxUnit + i;
     const int lane = 4 * (i >> 7) + ((i >> 4) & 3), j = i & 15, run = (i >> 6) & 1;
     reinterpret_cast<float *>(&f[j >> 1][lane])[2 * (j & 1) + run] = col < K ? of(col) : 1.0f;

@@ -465,7 +465,10 @@ cudaError_t run_split(const Mx4MatmulArgs &a, MxGemmArgs g, int smem_max, cudaSt
   if (!make_map(&wmap, a.w_codes, a.M, a.K, 128) || !make_map(&xmap, a.x_codes, a.T, a.K, NT))
     return cudaErrorInvalidValue;
   // Splits: the power of two that minimises waves x (steps of a CTA + 4, the
-  // steps' worth of a CTA's start and end).
+  // steps' worth of a CTA's start and end). One CTA per SM with all its memory:
+  // two with half of it, and twice the splits, were slower (37 tokens x 13824 x
+  // 5120: 16 us, 22 in halves; 128 tokens: 18 and 37, most of it for adding the
+  // parts).
   const int64_t tiles = (a.M + 127) / 128, steps = (a.K + kBK - 1) / kBK;
   int64_t best = INT64_MAX;
   for (int sp = 1; sp <= 8 && sp <= steps; sp *= 2) {
