@@ -41,8 +41,8 @@ namespace {
 constexpr int kMxWarps = 4;         // warps per CTA
 // Warps that an SM is meant to hold: 16 (128 registers) for the quantisation of
 // prepared rows (11008 x 4096 bf16, b = 128: 71 us; 20 warps the same, 24 spill: 84),
-// 24 for the kernels without the error bound (values of the same matrix
-// decoded: 29 us at 16, 27 at 24).
+// and for decoding rotated ones, 24 for the kernels that neither bound an error
+// nor rotate (values of the same matrix decoded: 29 us at 16, 27 at 24).
 constexpr int kMxResident = 16, kMxResidentPlain = 24;
 constexpr int kMxUnit = 1024;       // columns per warp pass: 32 lanes x 32 columns
 
@@ -68,9 +68,8 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *v) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
-// eight e2m1 codes -> floats
-__device__ __forceinline__ void floats_of_e2m1x8(uint32_t w, float *v) {
-  uint32_t h[4];
+// eight e2m1 codes -> four pairs of fp16 (exact)
+__device__ __forceinline__ void halves_of_e2m1x8(uint32_t w, uint32_t *h) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
@@ -79,12 +78,6 @@ __device__ __forceinline__ void floats_of_e2m1x8(uint32_t w, float *v) {
       "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
 }
 
 // 2^(b - 127) for a scale byte: 0 is the subnormal 2^-127, 255 is NaN
@@ -561,25 +554,23 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *p, int vec, const float (
   }
 }
 
-// x = d (.) (H_b q 2^e) / (sqrt(b) s) (times s for divided rows): fp32
-// arithmetic, one rounding to the output type, like the codec's own decode.
-// Without a rotation and a scale every value is exact in either type. Lanes
-// hold what they hold in the quantisation; the column factor d / (sqrt(b) s) is
-// formed once for all rows of the warp.
+// x = d (.) (H_b q 2^e) / (sqrt(b) s) (times s for divided rows): one rounding
+// to the output type at the end, like the codec's own decode; without a
+// rotation and a scale every value is exact in either type. Lanes hold what
+// they hold in the quantisation. Block bits 0-4 stay inside a group, whose
+// values share a scale: their sums (at most 32 x 6, in halves) are exact in
+// fp16, two columns an instruction and two an exchange between lanes. Then the
+// scale, and the other bits in fp32. What bounds the kernel is the exchanges:
+// 5120 x 13824 at b = 256 took 59 us with all bits in fp32 and the factors in
+// shared memory (L1 pipe 81% busy).
 template <typename T, int LB>
-__global__ void __launch_bounds__(32 * kMxWarps, kMxResidentPlain / kMxWarps) mx4_decode_kernel(const __grid_constant__ MxDecodeArgs p) {
+__global__ void __launch_bounds__(32 * kMxWarps, (LB > 0 ? kMxResident : kMxResidentPlain) / kMxWarps)
+    mx4_decode_kernel(const __grid_constant__ MxDecodeArgs p) {
   const int lane = threadIdx.x & 31;
   const int64_t unit = blockIdx.x % p.units_k, rg = (blockIdx.x / p.units_k) * kMxWarps + (threadIdx.x >> 5);
   const LanePlace at(unit, lane);
   const int64_t k_tiles = (p.K + 127) / 128;
   const bool in0 = at.run0 < p.K, in1 = at.run0 + 64 < p.K;
-  const float inv = (float)(1.0 / sqrt((double)(1 << LB)));
-  __shared__ Factors f;
-  form_factors(f, unit, p.K, [&](int64_t col) {
-    float v = inv;
-    if (p.s != nullptr) v = p.divide ? __fmul_rn(inv, p.s[col]) : __fdiv_rn(inv, p.s[col]);
-    return (LB > 0 && mask_is_negative(p.seed, col)) ? -v : v;
-  });
   uint2 c0 = make_uint2(0u, 0u), c1 = make_uint2(0u, 0u);
   uint32_t sw = 0;                    // the scale bytes of four groups, two of them this lane's
   auto fetch = [&](int64_t row) {
@@ -591,22 +582,63 @@ __global__ void __launch_bounds__(32 * kMxWarps, kMxResidentPlain / kMxWarps) mx
     if (in1) c1 = *reinterpret_cast<const uint2 *>(q + 32);
   };
   if (rg < p.M) fetch(rg);
+  const float inv = (float)(1.0 / sqrt((double)(1 << LB)));
+  __shared__ Factors shared;
+  form_factors(shared, unit, p.K, [&](int64_t col) {
+    float v = inv;
+    if (p.s != nullptr) v = p.divide ? __fmul_rn(inv, p.s[col]) : __fdiv_rn(inv, p.s[col]);
+    return (LB > 0 && mask_is_negative(p.seed, col)) ? -v : v;
+  });
+  float2 f[LB > 0 ? 16 : 1];          // in registers where the exchanges keep the L1 pipe busy
+  if constexpr (LB > 0) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f[j] = factor(shared, lane, j);
+  }
   for (int64_t row = rg; row < p.M; row += p.row_groups) {
-    float u[16], v[16];
-    floats_of_e2m1x8(c0.x, u);
-    floats_of_e2m1x8(c0.y, u + 8);
-    floats_of_e2m1x8(c1.x, v);
-    floats_of_e2m1x8(c1.y, v + 8);
+    __half2 h[16];                    // (run 0, run 1) of column j
+    {
+      uint32_t a[8], b[8];
+      halves_of_e2m1x8(c0.x, a);
+      halves_of_e2m1x8(c0.y, a + 4);
+      halves_of_e2m1x8(c1.x, b);
+      halves_of_e2m1x8(c1.y, b + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t lo = __byte_perm(a[i], b[i], 0x5410), hi = __byte_perm(a[i], b[i], 0x7632);
+        h[2 * i] = *reinterpret_cast<const __half2 *>(&lo);
+        h[2 * i + 1] = *reinterpret_cast<const __half2 *>(&hi);
+      }
+    }
     const uint32_t sh = 4 * (lane & 2);
     const float2 g = make_float2(e8m0_value((sw >> sh) & 255u), e8m0_value((sw >> (16 + sh)) & 255u));
     if (row + p.row_groups < p.M) fetch(row + p.row_groups);
+#pragma unroll
+    for (int t = 0; t < (LB < 4 ? LB : 4); ++t) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if ((j & (1 << t)) == 0) {
+          const __half2 a = h[j], b = h[j | (1 << t)];
+          h[j] = __hadd2(a, b);
+          h[j | (1 << t)] = __hsub2(a, b);
+        }
+      }
+    }
+    if constexpr (LB > 4) {
+      const __half2 s = __float2half2_rn((lane & 1) ? -1.0f : 1.0f);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) h[j] = __hfma2(h[j], s, __shfl_xor_sync(0xffffffffu, h[j], 1));
+    }
     float2 x[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = mul2(make_float2(u[j], v[j]), g);
-    rotate<LB>(x, lane);
+    for (int j = 0; j < 16; ++j) x[j] = mul2(__half22float2(h[j]), g);
+    if constexpr (LB > 6) butterflies_pair(x);
+    if constexpr (LB > 5) butterflies_lane(x, lane, 2);
+#pragma unroll
+    for (int t = 7; t < LB; ++t) butterflies_lane(x, lane, 1 << (t - 5));
+    float u[16], v[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const float2 y = mul2(x[j], factor(f, lane, j));
+      const float2 y = mul2(x[j], LB > 0 ? f[LB > 0 ? j : 0] : factor(shared, lane, j));
       u[j] = y.x;
       v[j] = y.y;
     }
@@ -711,7 +743,7 @@ cudaError_t launch_mx4_decode(const Mx4DecodeArgs &a, cudaStream_t s) {
   p.units_k = (a.K + kMxUnit - 1) / kMxUnit;
   const int es = a.out_t == QAMW_BF16 ? 2 : 4;
   p.vec = vector_bytes(a.out, a.ldo * es);
-  p.row_groups = row_groups_for(a.M, p.units_k, kMxResidentPlain);
+  p.row_groups = row_groups_for(a.M, p.units_k, a.log2b > 0 ? kMxResident : kMxResidentPlain);
   const dim3 grid((unsigned)(p.units_k * (p.row_groups / kMxWarps)));
   with_log2b(a.log2b, [&](auto lb) {
     if (a.out_t == QAMW_BF16) mx4_decode_kernel<__nv_bfloat16, decltype(lb)::value><<<grid, 32 * kMxWarps, 0, s>>>(p);
