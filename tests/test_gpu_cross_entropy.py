@@ -340,6 +340,31 @@ def test_runs_on_a_given_stream():
     assert torch.equal(loss, ref[0]) and torch.equal(dX, rX) and torch.equal(dW, rW)
 
 
+def test_offsets_beyond_32_bits():
+    """A head of more than 2^32 bytes: the normaliser, targets at its end, and the last rows of dW."""
+    T, K, V, tail = 3, 4096, 600000, 500
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    W = torch.empty((V, K), dtype=torch.bfloat16, device="cuda")
+    W.normal_(std=0.02, generator=gen)
+    X = torch.randn((T, K), device="cuda", generator=gen).to(torch.bfloat16)
+    t = torch.tensor([V - 1, V - 200, 5], device="cuda")
+    g = torch.tensor([0.5, 0.25, -0.5], device="cuda")
+    z = torch.cat([X.double() @ W[i:i + 50000].double().t() for i in range(0, V, 50000)], dim=1)
+    lse64 = torch.logsumexp(z, dim=1)
+    loss, lse = qamw.cross_entropy(X, W, t)
+    # |logits| < 8, |x w| sums below 100: the bounds of the header with S = 100
+    E = (K / 16 + 2) * 2.0 ** -22 * 100 + _tail(V, lse64) + 2.0 ** -21
+    assert ((lse - lse64).abs() <= E).all()
+    assert ((loss - (lse64 - z.gather(1, t[:, None])[:, 0])).abs() <= 2 * E).all()
+    dX, dW = qamw.cross_entropy_grad(X, W, t, lse, g)
+    G = torch.exp(z[:, V - tail:] - lse64[:, None])
+    G[0, tail - 1] -= 1
+    G[1, tail - 200] -= 1
+    G = G * g.double()[:, None]
+    tol = 2.0 ** -7 * (G.abs().t() @ X.double().abs()) + 2.0 ** -20 * X.double().abs().sum(0)
+    assert ((dW[V - tail:].double() - G.t() @ X.double()).abs() <= tol).all()
+
+
 def test_refusals():
     X, W, t, g = _case(8, 64, 300, 51)
     lse = torch.zeros(8, device="cuda")

@@ -273,6 +273,64 @@ def test_runs_on_a_given_stream():
     assert torch.equal(Y, qamw.mx4_linear(q, W))
 
 
+def test_offsets_beyond_32_bits():
+    """More than 2^32 bytes of input: the last rows equal those of a slice coded alone."""
+    M, K, tail = 70000, 32768, 200
+    W = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    W.normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    q = qamw.mx4_quantize(W, 128, 5)
+    part = qamw.mx4_quantize(W[M - tail:], 128, 5)
+    assert torch.equal(q.codes[M - tail:], part.codes)
+    assert torch.equal(qamw.mx4_scale_rows(q)[M - tail:], qamw.mx4_scale_rows(part))
+    D = qamw.mx4_decode(q, out=W)
+    assert torch.equal(D[M - tail:], qamw.mx4_decode(part))
+    X = torch.randn((3, K), device="cuda").to(torch.bfloat16)
+    Y, Yp = qamw.mx4_linear(q, X), qamw.mx4_linear(part, X)
+    tol = (K / 32 + 2) * 2.0 ** -22 * (_values(qamw.mx4_quantize(X, 128, 5)).abs() @ _values(part).abs().t())
+    assert ((Y[:, M - tail:] - Yp).abs() <= 2 * tol).all()
+
+
+@pytest.mark.parametrize("kind", ["ties", "zeros", "constant", "tiny", "huge", "wide"])
+@pytest.mark.parametrize("block", [0, 16, 64, 256])
+def test_quantize_hard_rows(kind, block):
+    """Rows that leave the fp32 decision open: exact ties of small integers, rows
+    and groups of zeros, one rotated coefficient, magnitudes near the ends of
+    fp32, and 2^40 between the columns."""
+    M, K = 140, 1280
+    g = np.random.default_rng(len(kind) + block)
+    W = g.integers(-6, 7, (M, K)).astype(np.float64) * 0.25
+    if kind == "zeros":
+        W[g.random((M, K)) < 0.97] = 0.0
+        W[:, 256:512] = 0.0
+    elif kind == "constant":
+        W[:] = g.standard_normal((M, 1))
+    elif kind == "tiny":
+        W = g.standard_normal((M, K)) * 2.0 ** -140
+    elif kind == "huge":
+        W = np.clip(g.standard_normal((M, K)), -3, 3) * 2.0 ** 124
+    elif kind == "wide":
+        W = g.standard_normal((M, K)) * 2.0 ** g.integers(-20, 21, (1, K))
+    t = torch.from_numpy(W.astype(np.float32))
+    s = _scale(K, 9)
+    for sd, divide in ((None, False), (s, False), (s, True)):
+        q = qamw.mx4_quantize(t.cuda(), block, 3, None if sd is None else torch.from_numpy(sd).cuda(), divide=divide)
+        _check_quantized(q, t.to(torch.float64).numpy(), sd, divide, block, 3)
+
+
+@pytest.mark.parametrize("value", [0.0, 2.0 ** -120, 2.0 ** 120, -1.5, float("inf")])
+def test_quantize_unusual_scales(value):
+    """Column scales far from 1, negative, zero or infinite: still the fp64 definition."""
+    M, K = 9, 256
+    t, W64 = _matrix(M, K, 5, torch.float32)
+    s = _scale(K, 2)
+    s[40:44] = value
+    sd = torch.from_numpy(s).cuda()
+    for divide in (False, True):
+        for block in (0, 64):
+            with np.errstate(all="ignore"):
+                _check_quantized(qamw.mx4_quantize(t.cuda(), block, 1, sd, divide=divide), W64, s, divide, block, 1)
+
+
 def test_refusals():
     W = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
     q = qamw.mx4_quantize(W)
