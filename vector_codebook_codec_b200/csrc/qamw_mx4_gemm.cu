@@ -129,14 +129,29 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const int all = (int)((g.K + kBK - 1) / kBK);
   const int k0 = rank * g.steps_per_split, k1 = min(k0 + g.steps_per_split, all);   // never empty
 
-  if (threadIdx.x == 0) {
-    fail_flag = 0;
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+  auto sf_bytes = [&](int k) { return (uint32_t)(g.k_tiles - 2 * k >= 2 ? 2 * kSfTile : kSfTile); };
+  auto load_w = [&](int k, uint32_t s) {
+    if (tc::elect_one()) {
+      mbar_arrive_expect_tx(&full[s], L::kA + L::kB + 2 * sf_bytes(k));
+      tc::load_2d(sA + (size_t)s * L::kA, &wmap, k * kRowBytes, (int)(mt * 128), &full[s]);
+      tc::load_bulk(sF + (size_t)s * 2 * L::kSf, g.w_scales + (mt * g.k_tiles + 2 * k) * kSfTile, sf_bytes(k),
+                    &full[s]);
     }
-    mbar_init(&acc_full, 1);
-    tc::mbar_init_fence();
+  };
+  const int n = k1 - k0, early = min(n, S);
+  if (warp == 0) {
+    if (lane == 0) {
+      fail_flag = 0;
+      for (int i = 0; i < S; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], 1);
+      }
+      mbar_init(&acc_full, 1);
+      tc::mbar_init_fence();
+    }
+    __syncwarp();
+    // the weights of the first stages are on their way while the CTA sets up and x is still being coded
+    for (int i = 0; i < early; ++i) load_w(k0 + i, i);
   }
   if (warp == 1) tc::alloc(&tmem_slot, L::kCols);
   tc::fence_before();
@@ -146,15 +161,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   uint32_t bad = 0;
 
   if (warp == 0) {
-    auto sf_bytes = [&](int k) { return (uint32_t)(g.k_tiles - 2 * k >= 2 ? 2 * kSfTile : kSfTile); };
-    auto load_w = [&](int k, uint32_t s) {
-      if (tc::elect_one()) {
-        mbar_arrive_expect_tx(&full[s], L::kA + L::kB + 2 * sf_bytes(k));
-        tc::load_2d(sA + (size_t)s * L::kA, &wmap, k * kRowBytes, (int)(mt * 128), &full[s]);
-        tc::load_bulk(sF + (size_t)s * 2 * L::kSf, g.w_scales + (mt * g.k_tiles + 2 * k) * kSfTile, sf_bytes(k),
-                      &full[s]);
-      }
-    };
     auto load_x = [&](int k, uint32_t s) {
       if (tc::elect_one()) {
         tc::load_2d(sB + (size_t)s * L::kB, &xmap, k * kRowBytes, 0, &full[s]);
@@ -162,9 +168,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
                       &full[s]);
       }
     };
-    // the weights of the first stages are on their way while x is still being coded
-    const int n = k1 - k0, early = min(n, S);
-    for (int i = 0; i < early; ++i) load_w(k0 + i, i);
     if (g.after_quantize) tc::griddep_wait();
     for (int i = 0; i < early; ++i) load_x(k0 + i, i);
     int it = early;
@@ -232,10 +235,23 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     __syncwarp();
     tc::cluster_sync();
     if (warp >= 2) {
-      for (int64_t t = rank; t < g.T; t += g.splits) {
-        float v = 0.0f;
-        for (int r = 0; r < g.splits; ++r) v += tc::ld_cluster(tc::address_in(&part[t * 128 + 32 * wq + lane], r));
-        put(t, v);
+      // four tokens' parts of up to 8 ranks in flight together, added in the order of the ranks
+      for (int64_t t0 = rank; t0 < g.T; t0 += 4 * g.splits) {
+        float v[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t t = t0 + i * g.splits;
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            v[i][r] = r < g.splits && t < g.T ? tc::ld_cluster(tc::address_in(&part[t * 128 + 32 * wq + lane], r)) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float sum = v[i][0];
+#pragma unroll
+          for (int r = 1; r < 8; ++r) sum += v[i][r];   // a rank that is not there adds 0
+          put(t0 + i * g.splits, sum);
+        }
       }
     }
     __syncwarp();
