@@ -390,7 +390,8 @@ size_t qamw_decode_matmul_workspace_bytes(int64_t M, int64_t K, int64_t T);
  * scales uint8 [ceil(M/128)][ceil(K/128)][512], byte (r % 32) * 16 + (r / 32)
  * * 4 + g of a tile for its row r and group g of 4 (the layout in which the
  * tensor cores take scales; padding bytes are 0): qamw_mx4_scale_bytes(M, K)
- * bytes. K is a multiple of 32; codes and scales are 16-byte aligned.
+ * bytes. K is a multiple of 32 and at most 2^24, rows at most 2^30; codes and
+ * scales are 16-byte aligned.
  */
 #define QAMW_MX4_GROUP 32
 /* Bytes of the scales of an M x K matrix (0 if the shape is invalid). */

@@ -309,6 +309,7 @@ ODD = ctypes.c_void_p(0x10001)
     (_mxq, dict(block=96), QAMW_EINVAL), (_mxq, dict(block=512), QAMW_EINVAL),
     (_mxq, dict(block=2048, K=2048, ldw=2048), QAMW_EUNSUPPORTED), (_mxq, dict(W=ODD), QAMW_EINVAL),
     (_mxq, dict(codes=ODD), QAMW_EINVAL), (_mxq, dict(M=(1 << 30) + 1), QAMW_EUNSUPPORTED),
+    (_mxq, dict(K=(1 << 24) + 32, ldw=1 << 25, block=32), QAMW_EUNSUPPORTED),
     (_mxd, dict(codes=None), QAMW_ENULL), (_mxd, dict(out=None), QAMW_ENULL), (_mxd, dict(ot=9), QAMW_EINVAL),
     (_mxd, dict(ldo=200), QAMW_EINVAL), (_mxd, dict(block=-2), QAMW_EINVAL), (_mxd, dict(scales=ODD), QAMW_EINVAL),
     (_mxd, dict(out=ODD), QAMW_EINVAL),

@@ -626,7 +626,7 @@ static int check_mx4(int64_t M, int64_t K, const char *fn) {
   if (M < 1) return fail(QAMW_EINVAL, "%s: the number of rows must be >= 1 (got %lld)", fn, (long long)M);
   if (K < QAMW_MX4_GROUP || K % QAMW_MX4_GROUP)
     return fail(QAMW_EINVAL, "%s: K must be a positive multiple of %d (got %lld)", fn, QAMW_MX4_GROUP, (long long)K);
-  if (M > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return fail(QAMW_EUNSUPPORTED, "%s: shape too large", fn);
+  if (M > (int64_t(1) << 30) || K > (int64_t(1) << 24)) return fail(QAMW_EUNSUPPORTED, "%s: shape too large", fn);
   return QAMW_OK;
 }
 
@@ -651,7 +651,7 @@ static bool element_aligned(const void *p, qamw_dtype t) {
 }
 
 size_t qamw_mx4_scale_bytes(int64_t M, int64_t K) {
-  if (M < 1 || K < QAMW_MX4_GROUP || K % QAMW_MX4_GROUP || M > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return 0;
+  if (M < 1 || K < QAMW_MX4_GROUP || K % QAMW_MX4_GROUP || M > (int64_t(1) << 30) || K > (int64_t(1) << 24)) return 0;
   return mx4_scale_bytes(M, K);
 }
 

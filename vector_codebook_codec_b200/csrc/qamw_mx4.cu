@@ -333,7 +333,9 @@ __device__ __forceinline__ void rotate(float2 (&x)[16], int lane) {
 }
 
 // PREP: a channel scale or a rotation (blocks of 2^LB columns); otherwise the
-// values are exact as read.
+// values are exact as read. 11008 x 4096 bf16: 65 us at b = 128 with a scale
+// (1.75 TB/s; 760 instructions per 1024 values, 240 of them on the integer pipe
+// at half rate, 16 warps per SM), 23 us plain (5 TB/s).
 template <typename T, bool PREP, int LB>
 __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxResidentPlain) / kMxWarps)
     mx4_quantize_kernel(const __grid_constant__ MxQuantArgs p) {

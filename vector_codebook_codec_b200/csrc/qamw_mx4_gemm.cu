@@ -12,9 +12,14 @@
 //  - up to 128 tokens: a CTA's tile is 128 weight rows (the tensor-memory
 //    lanes) by NT tokens; the weights are all there is to read, so the columns
 //    are split over a cluster until the SMs are busy, and the parts are added
-//    in shared memory in the order of the ranks;
+//    in shared memory in the order of the ranks. 37 tokens x 13824 x 5120: 11 us
+//    (3.5 TB/s with its start and end), 1 token x 4096 x 4096: 5 us;
 //  - more tokens: a pair of CTAs (cta_group::2) takes 256 tokens x 256 weight
-//    rows, persistent. A token is a lane, so its outputs are contiguous.
+//    rows, persistent. A token is a lane, so its outputs are contiguous. 4096
+//    tokens x 11008 x 4096: 78 us (4.7 PFLOP/s), x 16384 columns: 93 us (5.9);
+//    a step's MMAs take 594 of 512 nominal cycles whether or not anything is
+//    loaded, and the accumulator's drain 1.3 of 13 thousand cycles a tile: two
+//    of 256 columns and the scales do not fit tensor memory together.
 #include <algorithm>
 
 #include "qamw_device.cuh"
