@@ -43,6 +43,7 @@ constexpr int kThreads = 320;     // warp 0: loads, warp 1: MMA, warps 2-9: epil
 constexpr int kHalf = 128;        // columns of a tile that an epilogue warp takes
 constexpr int kBox = 64 * 128;    // bytes of a 64 x 64 box
 constexpr int kMaxStages = 8;
+constexpr int kShortDepth = 256;  // contraction up to which bf16 outputs leave by TMA stores (see run())
 constexpr int kGroupRows = 16;    // row tiles walked together (their operand stays in L2)
 
 enum Epilogue { kStats = 0, kGrad = 1, kStore = 2, kSlot = 3 };
@@ -64,6 +65,7 @@ struct CeArgs {
   const float *factor;            // kGrad: of G (divided out); kStore: of D
   __nv_bfloat16 *out;             // kGrad: G, kStore: D
   int64_t ldo;
+  int tma_out;                    // they leave by TMA stores
   float *slots;                   // kSlot: [splits][rows][cols] fp32
   int add;                        // kSlot: add to the slots instead of writing them
 };
@@ -137,7 +139,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A_MN / B_MN: the operand lies [contraction][rows or columns] in memory.
 template <int CTAS, bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
-    ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, CeArgs g) {
+    ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                   const __grid_constant__ CUtensorMap omap, CeArgs g) {
   using L = CeTile<CTAS>;
   tc::griddep_launch_dependents();   // the next kernel may set up; it waits for this one before it reads or writes
   extern __shared__ uint8_t smem_raw[];
@@ -294,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t buf = seg & 1u;
       if (!tc::wait_warp(&acc_full[buf], (seg >> 1) & 1u, fail)) { bad |= QAMW_STATUS_TIMEOUT; break; }
       tc::fence_after();
+      uint8_t *tile = sB + S * L::kB + (warp - 2) * tc::kOutBytes;   // this warp's, where the outputs are bf16
       const uint32_t taddr = tmem + buf * kBN + kHalf * half + ((uint32_t)(32 * wq) << 16);
       float buffer[2][32];
       if (n_cols > 0) tc::ld32_async(taddr, buffer[0]);
@@ -341,7 +345,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j) v[j] *= scale;
         }
         if constexpr (EPI == kGrad || EPI == kStore) {
-          if (in) tc::store_row32(g.out + row * g.ldo + col0 + c, n, v);
+          if (g.tma_out) {
+            if ((q & 1) == 0) {
+              if (lane == 0) tc::stores_read();
+              __syncwarp();
+            }
+            tc::stage_row32(tile, q & 1, v);
+            // 64 columns, or the last of them; a warp past the last row has nothing to store
+            if (((q & 1) != 0 || c + 32 >= n_cols) && row - lane < g.rows)
+              tc::store_tile(tile, &omap, (int)col0 + 32 * (q & ~1), (int)(row - lane));
+          } else if (in) {
+            tc::store_row32(g.out + row * g.ldo + col0 + c, n, v);
+          }
         }
         if constexpr (EPI == kSlot) {
           if (in) {   // cols % 8 == 0: 16-byte groups are all in or all out
@@ -369,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++seg;
     }
+    if ((EPI == kGrad || EPI == kStore) && lane == 0) tc::stores_done();
   }
 
   __syncwarp();
@@ -521,8 +537,19 @@ cudaError_t run(const Operand &A, const Operand &B, CeArgs g, cudaStream_t s) {
   if ((e = cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
   g.n_r = (g.rows + L::kRows - 1) / L::kRows;
   g.n_c = (g.cols + kBN - 1) / kBN;
-  g.stages = (int)std::min<int64_t>(kMaxStages, (smem_max - 2048) / (g.a_bytes + L::kB));
-  const size_t smem = 1024 + (size_t)g.stages * (g.a_bytes + L::kB);
+  // A lane holds a row of the accumulator, and 32 lanes that store to 32 rows
+  // keep the L1 pipe busy (69% in dW of 301 tokens). Where a tile has few steps,
+  // bf16 outputs are laid out in shared memory and leave by TMA stores instead
+  // (gradient of 16 tokens x 32000 x 2048 99 -> 91 us, of 128 tokens 109 -> 101);
+  // with more steps the stage of loads that this memory costs is worth more (512
+  // tokens 177 -> 183, 4096 x 65536 x 4096 4.11 -> 4.17 ms).
+  CUtensorMap omap = amap;
+  const bool bf16_out = (EPI == kGrad || EPI == kStore) && g.depth <= kShortDepth;
+  g.tma_out = bf16_out && reinterpret_cast<uintptr_t>(g.out) % 16 == 0 && g.ldo % 8 == 0;
+  if (g.tma_out && !make_map(&omap, g.out, g.rows, g.cols, g.ldo, 32, 64)) return cudaErrorInvalidValue;
+  const int64_t out_bytes = bf16_out ? 8 * tc::kOutBytes : 0;
+  g.stages = (int)std::min<int64_t>(kMaxStages, (smem_max - 2048 - out_bytes) / (g.a_bytes + L::kB));
+  const size_t smem = 1024 + (size_t)g.stages * (g.a_bytes + L::kB) + (size_t)out_bytes;
   auto kern = ce_gemm_kernel<CTAS, A_MN, B_MN, EPI>;
   if ((e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -539,7 +566,7 @@ cudaError_t run(const Operand &A, const Operand &B, CeArgs g, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, amap, bmap, g);
+  return cudaLaunchKernelEx(&cfg, kern, amap, bmap, omap, g);
 }
 
 // One CTA per tile, or a pair. A step of either takes the same time, so the

@@ -223,6 +223,38 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16 *o, int n, const float
   }
 }
 
+// ---- tiles back to device memory (a warp's 32 rows x 64 bf16 columns) ----
+constexpr int kOutBytes = 32 * 128;   // 128-byte swizzle: 16-byte piece p of row r lies at piece p ^ (r % 8)
+// 32 columns of the lane's row: pieces 4 * half .. 4 * half + 3
+__device__ __forceinline__ void stage_row32(uint8_t *tile, int half, const float *v) {
+  const int r = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(tile + r * 128 + (((4 * half + i) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// The warp's tile out by one TMA store (rows and columns past the tensor's end
+// are not written); by all lanes, once they have written the tile.
+__device__ __forceinline__ void store_tile(const uint8_t *tile, const CUtensorMap *map, int x, int y) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(smem_u32(tile))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+// until the lane's stores have read their tiles / are done
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // Tensor-memory allocation by one whole warp; `cols` a power of two >= 32.
 __device__ __forceinline__ void alloc(uint32_t *slot, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
