@@ -509,6 +509,20 @@ int qamw_cross_entropy_grad_piece(const void *X, int64_t T, int64_t K, int64_t l
                                   qamw_stream_t stream);
 int qamw_cross_entropy_grad_finish(int64_t T, int64_t K, int64_t piece, void *dX, int64_t lddx, void *workspace,
                                    size_t workspace_bytes, qamw_stream_t stream);
+/*
+ * The same in one call for a head whose bf16 rows all lie in memory (W: device
+ * bf16 [V][ldw]): qamw_cross_entropy is the piece [0, V) and the finish;
+ * qamw_cross_entropy_grad walks pieces of `piece` entries (a multiple of
+ * QAMW_VOCAB_TILE, or at least V) and finishes. Results equal those of the
+ * calls above bit for bit.
+ */
+int qamw_cross_entropy(const void *X, int64_t T, int64_t K, int64_t ldx, const void *W, int64_t V, int64_t ldw,
+                       const int64_t *targets, int64_t ignore_index, float *loss, float *lse, void *workspace,
+                       size_t workspace_bytes, int32_t *status, qamw_stream_t stream);
+int qamw_cross_entropy_grad(const void *X, int64_t T, int64_t K, int64_t ldx, const void *W, int64_t V, int64_t ldw,
+                            const int64_t *targets, int64_t ignore_index, const float *lse, const float *grad_loss,
+                            int64_t piece, void *dX, int64_t lddx, void *dW, int64_t lddw, void *workspace,
+                            size_t workspace_bytes, int32_t *status, qamw_stream_t stream);
 
 /*
  * qamw_rotate_rows -- the rotation alone, for tests of step (2).

@@ -383,6 +383,40 @@ def _cex(lib, **kw):
     return lib.qamw_cross_entropy_grad_finish(*a.values(), None)
 
 
+def _cew(lib, **kw):
+    a = dict(X=FAKE, T=8, K=64, ldx=64, W=FAKE, V=300, ldw=64, t=FAKE, ignore=-100, loss=FAKE, lse=FAKE, ws=FAKE, wb=BIG)
+    a.update(kw)
+    return lib.qamw_cross_entropy(*a.values(), None, None)
+
+
+def _cgw(lib, **kw):
+    a = dict(X=FAKE, T=8, K=64, ldx=64, W=FAKE, V=300, ldw=64, t=FAKE, ignore=-100, lse=FAKE, g=FAKE, piece=300, dX=FAKE,
+             lddx=64, dW=None, lddw=0, ws=FAKE, wb=BIG)
+    a.update(kw)
+    return lib.qamw_cross_entropy_grad(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("call", [_cew, _cgw])
+@pytest.mark.parametrize("kw,rc", [
+    (dict(X=None), QAMW_ENULL), (dict(W=None), QAMW_ENULL), (dict(t=None), QAMW_ENULL), (dict(lse=None), QAMW_ENULL),
+    (dict(T=0), QAMW_EINVAL), (dict(K=60), QAMW_EINVAL), (dict(V=0), QAMW_EINVAL), (dict(ldx=60), QAMW_EINVAL),
+    (dict(ldw=68), QAMW_EINVAL), (dict(X=ODD), QAMW_EINVAL), (dict(ws=None), QAMW_EWORKSPACE),
+    (dict(wb=100), QAMW_EWORKSPACE), (dict(ws=ODD), QAMW_EINVAL), (dict(V=1 << 31), QAMW_EUNSUPPORTED),
+])
+def test_whole_cross_entropy_rejects_bad_arguments(lib, call, kw, rc):
+    assert call(lib, **kw) == rc
+    assert lib.qamw_last_error()
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(dX=None), QAMW_ENULL), (dict(g=None), QAMW_ENULL), (dict(lddx=63), QAMW_EINVAL), (dict(piece=0), QAMW_EINVAL),
+    (dict(piece=200), QAMW_EINVAL), (dict(dW=FAKE, lddw=63), QAMW_EINVAL), (dict(dW=ODD, lddw=64), QAMW_EINVAL),
+])
+def test_whole_gradient_rejects_bad_arguments(lib, kw, rc):
+    assert _cgw(lib, **kw) == rc
+    assert lib.qamw_last_error()
+
+
 @pytest.mark.parametrize("call", [_cep, _ceg])
 @pytest.mark.parametrize("kw,rc", [
     (dict(X=None), QAMW_ENULL), (dict(W=None), QAMW_ENULL), (dict(t=None), QAMW_ENULL), (dict(T=0), QAMW_EINVAL),

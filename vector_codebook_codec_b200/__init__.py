@@ -91,6 +91,10 @@ _SIGNATURES = {
                                                      _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i32, _c_p, _c_i64,
                                                      _c_p, _c_sz, _c_p, _c_p]),
     "qamw_cross_entropy_grad_finish": (ctypes.c_int, [_c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_sz, _c_p]),
+    "qamw_cross_entropy": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p,
+                                          _c_p, _c_sz, _c_p, _c_p]),
+    "qamw_cross_entropy_grad": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_p,
+                                               _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_sz, _c_p, _c_p]),
     "qamw_lloyd_workspace_bytes": (_c_sz, [_c_i64, _c_i32]),
     "qamw_lloyd_assign": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_p]),
     "qamw_lloyd_update": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i32, _c_p, _c_p, _c_sz, _c_p]),
@@ -180,6 +184,8 @@ qamw_cross_entropy_finish = _raw("qamw_cross_entropy_finish")
 qamw_cross_entropy_grad_workspace_bytes = _raw("qamw_cross_entropy_grad_workspace_bytes")
 qamw_cross_entropy_grad_piece = _raw("qamw_cross_entropy_grad_piece")
 qamw_cross_entropy_grad_finish = _raw("qamw_cross_entropy_grad_finish")
+qamw_cross_entropy = _raw("qamw_cross_entropy")
+qamw_cross_entropy_grad = _raw("qamw_cross_entropy_grad")
 
 
 # ---------------------------------------------------------------------------
@@ -555,11 +561,6 @@ def _raw_stream(device):
     return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
-def _run(name, rc):
-    if rc != QAMW_OK:
-        _check(name, rc)
-
-
 def _address(t):
     return None if t is None else t.data_ptr()
 
@@ -773,7 +774,7 @@ def mx4_linear(W: Mx4, X, out_dtype=None, status=None, stream=None, out=None):
             out, ld = torch.empty((T, M), dtype=out_dtype, device=device), M
         else:
             ld = _need_out("out", out, (T, M), out_dtype, device)
-        _run("qamw_mx4_linear", load_library().qamw_mx4_linear(
+        _check("qamw_mx4_linear", load_library().qamw_mx4_linear(
             W.codes.data_ptr(), W.scales.data_ptr(), M, X.data_ptr(), xt, T, K, ldx, _address(W.col_scale), W.block,
             W.seed & (2**64 - 1), out.data_ptr(), ot, ld, ws.data_ptr(), nws, _address(status), _raw_stream(device)))
     return out
@@ -881,22 +882,27 @@ def cross_entropy(X, head, targets, codebook=None, ignore_index: int = -100, pie
     rows at a time. ``targets`` is int64 [T]; ``ignore_index`` has loss 0."""
     torch = _torch()
     h, ldx, device = _ce_inputs(X, head, targets, codebook, status)
-    T, lib = X.shape[0], load_library()
-    rows = _piece_rows(h.V, piece, _DECODED_BYTES // (2 * h.K) if h.coded else h.V + VOCAB_TILE)
+    T, K, V, lib = X.shape[0], h.K, h.V, load_library()
+    if piece is not None or h.coded:
+        rows = _piece_rows(V, piece, _DECODED_BYTES // (2 * K))
+    nws = ((V + 127) // 128 * T * 8 + 255 & ~255) + (4 * T + 255 & ~255)   # qamw_cross_entropy_workspace_bytes(T, V)
     with _on(device, stream):
-        nws = int(lib.qamw_cross_entropy_workspace_bytes(T, h.V))
         ws = torch.empty(nws, dtype=torch.uint8, device=device)
         loss = torch.empty(T, dtype=torch.float32, device=device)
         lse = torch.empty(T, dtype=torch.float32, device=device)
         at, st, rs = targets.data_ptr(), _address(status), _raw_stream(device)
-        for v0 in range(0, h.V, rows):
-            n = min(rows, h.V - v0)
+        if piece is None and not h.coded:
+            _check("qamw_cross_entropy", lib.qamw_cross_entropy(
+                X.data_ptr(), T, K, ldx, head.data_ptr(), V, h.ld, at, ignore_index, loss.data_ptr(), lse.data_ptr(),
+                ws.data_ptr(), nws, st, rs))
+            return loss, lse
+        for v0 in range(0, V, rows):
+            n = min(rows, V - v0)
             W = h.rows(v0, n, status)
             _check("qamw_cross_entropy_piece", lib.qamw_cross_entropy_piece(
-                X.data_ptr(), T, h.K, ldx, W.data_ptr(), n, h.ld, v0, h.V, at, ignore_index, ws.data_ptr(), nws, st,
-                rs))
+                X.data_ptr(), T, K, ldx, W.data_ptr(), n, h.ld, v0, V, at, ignore_index, ws.data_ptr(), nws, st, rs))
         _check("qamw_cross_entropy_finish", lib.qamw_cross_entropy_finish(
-            T, h.V, at, ignore_index, ws.data_ptr(), nws, loss.data_ptr(), lse.data_ptr(), st, rs))
+            T, V, at, ignore_index, ws.data_ptr(), nws, loss.data_ptr(), lse.data_ptr(), st, rs))
     return loss, lse
 
 
@@ -923,6 +929,11 @@ def cross_entropy_grad(X, head, targets, lse, grad_loss, codebook=None, ignore_i
         dX = torch.empty((T, h.K), dtype=torch.bfloat16, device=device)
         dW = torch.empty((h.V, h.K), dtype=torch.bfloat16, device=device) if weight_grad else None
         at, st, rs = targets.data_ptr(), _address(status), _raw_stream(device)
+        if not h.coded:
+            _check("qamw_cross_entropy_grad", lib.qamw_cross_entropy_grad(
+                X.data_ptr(), T, h.K, ldx, head.data_ptr(), h.V, h.ld, at, ignore_index, lse.data_ptr(),
+                grad_loss.data_ptr(), rows, dX.data_ptr(), h.K, _address(dW), h.K, ws.data_ptr(), nws, st, rs))
+            return dX, dW
         for v0 in range(0, h.V, rows):
             n = min(rows, h.V - v0)
             W = h.rows(v0, n, status)

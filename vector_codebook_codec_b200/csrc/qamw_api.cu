@@ -884,6 +884,54 @@ int qamw_cross_entropy_grad_finish(int64_t T, int64_t K, int64_t piece, void *dX
   return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
 }
 
+int qamw_cross_entropy(const void *X, int64_t T, int64_t K, int64_t ldx, const void *W, int64_t V, int64_t ldw,
+                       const int64_t *targets, int64_t ignore_index, float *loss, float *lse, void *workspace,
+                       size_t workspace_bytes, int32_t *status, qamw_stream_t stream) {
+  static const char *fn = "qamw_cross_entropy";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  if (!loss || !lse) return fail(QAMW_ENULL, "%s: loss and lse must be non-NULL", fn);
+  CeArgsIn a{X, T, K, ldx, W, V, ldw, 0, V, targets, ignore_index, status};
+  if ((rc = check_ce_piece(a, fn))) return rc;
+  if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_workspace(T, V).total, fn))) return rc;
+  cudaError_t e = launch_ce_piece(a, workspace, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_ce_finish(a, workspace, loss, lse, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
+int qamw_cross_entropy_grad(const void *X, int64_t T, int64_t K, int64_t ldx, const void *W, int64_t V, int64_t ldw,
+                            const int64_t *targets, int64_t ignore_index, const float *lse, const float *grad_loss,
+                            int64_t piece, void *dX, int64_t lddx, void *dW, int64_t lddw, void *workspace,
+                            size_t workspace_bytes, int32_t *status, qamw_stream_t stream) {
+  static const char *fn = "qamw_cross_entropy_grad";
+  CallRange nvtx_range(fn);
+  g_last_error[0] = 0;
+  int rc;
+  if (!lse || !grad_loss || !dX) return fail(QAMW_ENULL, "%s: lse, grad_loss and dX must be non-NULL", fn);
+  CeArgsIn a{X, T, K, ldx, W, V, ldw, 0, V, targets, ignore_index, status};
+  if ((rc = check_ce_piece(a, fn))) return rc;
+  if (piece < 1 || piece > (int64_t(1) << 30) || (piece < V && piece % QAMW_VOCAB_TILE))
+    return fail(QAMW_EINVAL, "%s: piece (%lld) must be a positive multiple of %d, or at least V", fn, (long long)piece,
+                QAMW_VOCAB_TILE);
+  if (lddx < K || reinterpret_cast<uintptr_t>(dX) % 2)
+    return fail(QAMW_EINVAL, "%s: lddx (%lld) must be >= K and dX 2-byte aligned", fn, (long long)lddx);
+  if (dW != nullptr && (lddw < K || reinterpret_cast<uintptr_t>(dW) % 2))
+    return fail(QAMW_EINVAL, "%s: lddw (%lld) must be >= K and dW 2-byte aligned", fn, (long long)lddw);
+  if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_grad_workspace(T, K, piece).total, fn))) return rc;
+  for (int64_t v0 = 0; v0 < V; v0 += piece) {
+    a.v0 = v0;
+    a.n = V - v0 < piece ? V - v0 : piece;
+    a.W = static_cast<const uint16_t *>(W) + v0 * ldw;
+    void *rows = dW == nullptr ? nullptr : static_cast<uint16_t *>(dW) + v0 * lddw;
+    const cudaError_t e = launch_ce_grad_piece(a, lse, grad_loss, piece, v0 == 0, rows, lddw, workspace,
+                                               (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, fn);
+  }
+  const cudaError_t e = launch_ce_grad_finish(T, K, piece, dX, lddx, workspace, (cudaStream_t)stream);
+  return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
+}
+
 int qamw_selftest_wait_timeout(uint32_t tries, int32_t *status, qamw_stream_t stream) {
   static const char *fn = "qamw_selftest_wait_timeout";
   CallRange nvtx_range(fn);
