@@ -11,7 +11,7 @@
 // decision, but the work is done in fp32: a value is computed with a bound m on
 // its error, and both y - m and y + m are rounded to 4 bits. Where they agree,
 // so does every value between them, the exact one among them. Where they
-// differ (about 2 in 10^5 values of Gaussian rows at b = 128), or the group's
+// differ (about 6 in 10^5 values of Gaussian rows at b = 128), or the group's
 // exponent hangs on the error, the warp forms the value in fp64 from the row.
 // An e2m1 border has at most three significant bits, so the exponent and the
 // top mantissa bits of that double, with a sticky bit for the rest, decide
@@ -19,10 +19,10 @@
 //
 // Error of the fp32 value, with A = sum of |v| over the block: v itself 2 x
 // 2^-24 (1/s rounded, and the product), one rounding of at most 2^-24 A per
-// butterfly level, the factor 2^-e / sqrt(b) and its product 2 x 2^-24, and the
-// sum y +- m one more: (log2 b + 5) 2^-24 A. A <= sqrt(b sum v^2) takes its
+// butterfly level, the factor 2^-e / sqrt(b) one and the sum y +- m, fused with
+// its product, one more: (log2 b + 4) 2^-24 A. A <= sqrt(b sum v^2) takes its
 // place: half the instructions, 1.25 times as large for Gaussian rows. The
-// factor is log2 b + 8 for the roundings of the bound itself.
+// factor used is log2 b + 6: the bound's own roundings are 10^-6 of it.
 //
 // A lane loads two runs of 16 columns, 64 columns apart, so that four lanes
 // read 128 contiguous bytes of bf16; block bits 0-3 and 6 are butterflies on
@@ -333,15 +333,21 @@ __device__ __forceinline__ void rotate(float2 (&x)[16], int lane) {
 }
 
 // PREP: a channel scale or a rotation (blocks of 2^LB columns); otherwise the
-// values are exact as read. 11008 x 4096 bf16: 65 us at b = 128 with a scale
-// (1.75 TB/s; 760 instructions per 1024 values, 240 of them on the integer pipe
-// at half rate, 16 warps per SM), 23 us plain (5 TB/s).
+// values are exact as read. 11008 x 4096 bf16: 62 us at b = 128 with a scale
+// (1.8 TB/s; 760 instructions per 1024 values, 240 of them on the integer pipe
+// at half rate, 16 warps per SM; 66 us with the rows dealt out beforehand), 23
+// us plain (5 TB/s).
 template <typename T, bool PREP, int LB>
 __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxResidentPlain) / kMxWarps)
     mx4_quantize_kernel(const __grid_constant__ MxQuantArgs p) {
   constexpr int N = Raw<T>::kWords;
   const int lane = threadIdx.x & 31;
-  const int64_t unit = blockIdx.x % p.units_k, rg = (blockIdx.x / p.units_k) * kMxWarps + (threadIdx.x >> 5);
+  const int64_t unit = blockIdx.x % p.units_k, first = blockIdx.x / p.units_k, ctas = p.row_groups / kMxWarps;
+  // The CTA's rows are first, first + ctas, ...; its warps take them in turn as
+  // they come free, since a row that needs fp64 takes several times as long.
+  __shared__ int taken;
+  if (threadIdx.x == 0) taken = kMxWarps;
+  const int64_t rg = first + (threadIdx.x >> 5) * ctas;
   const LanePlace at(unit, lane);
   const int64_t k_tiles = (p.K + 127) / 128, rows_pad = (p.M + 127) / 128 * 128;
   // K % 32 == 0: a run of 16 columns and a group are all in or all out
@@ -366,7 +372,12 @@ __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxReside
     });
   const float inv = (float)(1.0 / sqrt((double)(1 << LB)));
   uint32_t bad = 0;
-  for (int64_t row = rg; row < rows_pad; row += p.row_groups) {
+  if (!PREP) __syncthreads();   // `taken` is set (form_factors ends with a barrier too)
+  int64_t next;
+  for (int64_t row = rg; row < rows_pad; row = next) {
+    int turn = 0;
+    if (lane == 0) turn = atomicAdd(&taken, 1);
+    next = first + (int64_t)__shfl_sync(0xffffffffu, turn, 0) * ctas;
     uint32_t sword = 0;
     if (row < p.M) {
       float2 x[16];
@@ -380,7 +391,6 @@ __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxReside
         any0 &= drop;
         any1 &= drop;
       }
-      const int64_t next = row + p.row_groups;
       if (next < p.M) {               // the next row is on its way while this one is worked on
         load16<T>(src + next * p.ldw, p.vec, in[0], w0);
         load16<T>(src + next * p.ldw + 64, p.vec, in[1], w1);
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxReside
           top = make_float2(max_abs(top.x, x[j].x, x[j + 1].x), max_abs(top.y, x[j].y, x[j + 1].y));
         top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, 1));
         top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, 1));
-        constexpr float kBound = (float)(LB + 8) * 0x1p-24f;
+        constexpr float kBound = (float)(LB + 6) * 0x1p-24f;
         constexpr float kTerms = (float)(1 << (LB > 5 ? LB : 5));
         float2 scale, ms;             // 2^-e / sqrt(b) and m 2^-e of each run
         uint32_t again[2] = {0u, 0u}; // the run's values to be decided from fp64
