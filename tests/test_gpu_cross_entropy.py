@@ -365,6 +365,28 @@ def test_offsets_beyond_32_bits():
     assert ((dW[V - tail:].double() - G.t() @ X.double()).abs() <= tol).all()
 
 
+def test_two_streams_at_once():
+    """Forward and backward of two batches on two streams, beside 4-bit products on a third."""
+    a, b = _case(300, 256, 2000, 61), _case(40, 128, 3000, 62)
+    W = qamw.mx4_quantize(a[1], 64, 1)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    want = []
+    for X, H, t, g in (a, b):
+        loss, lse = qamw.cross_entropy(X, H, t)
+        want.append((loss, lse) + qamw.cross_entropy_grad(X, H, t, lse, g))
+    wanted = qamw.mx4_linear(W, a[0][:60])
+    torch.cuda.synchronize()
+    got, ys = [[], []], []
+    for _ in range(10):
+        for n, (X, H, t, g) in enumerate((a, b)):
+            loss, lse = qamw.cross_entropy(X, H, t, stream=streams[n])
+            got[n].append((loss, lse) + qamw.cross_entropy_grad(X, H, t, lse, g, stream=streams[n]))
+        ys.append(qamw.mx4_linear(W, a[0][:60], stream=streams[2]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for n in range(2) for r in got[n] for p, q in zip(r, want[n]))
+    assert all(torch.equal(y, wanted) for y in ys)
+
+
 def test_refusals():
     X, W, t, g = _case(8, 64, 300, 51)
     lse = torch.zeros(8, device="cuda")

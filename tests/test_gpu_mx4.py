@@ -331,6 +331,25 @@ def test_quantize_unusual_scales(value):
                 _check_quantized(qamw.mx4_quantize(t.cuda(), block, 1, sd, divide=divide), W64, s, divide, block, 1)
 
 
+def test_many_streams_at_once():
+    """Calls of every kernel on eight streams, interleaved: each as it is alone."""
+    cases = []
+    for i, (M, K, T) in enumerate([(300, 512, 1), (2048, 1024, 100), (640, 768, 20), (900, 512, 300), (4096, 512, 128),
+                                   (77, 2048, 64), (1500, 1024, 128), (256, 4096, 3)]):
+        W, _ = _matrix(M, K, i, torch.bfloat16)
+        X, _ = _matrix(T, K, 50 + i, torch.bfloat16)
+        q, x = qamw.mx4_quantize(W.cuda(), 64, i), X.cuda()
+        cases.append((q, x, qamw.mx4_linear(q, x), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[] for _ in cases]
+    for _ in range(20):
+        for n, (q, x, _, stream) in enumerate(cases):
+            got[n].append(qamw.mx4_linear(q, x, stream=stream))
+    torch.cuda.synchronize()
+    for n, (_, _, want, _) in enumerate(cases):
+        assert all(torch.equal(y, want) for y in got[n])
+
+
 def test_refusals():
     W = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
     q = qamw.mx4_quantize(W)

@@ -217,30 +217,33 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       else static_cast<float *>(g.Y)[t * g.ldy + m] = v;
     }
   };
-  if (g.splits == 1) {
-    if (warp >= 2) {
-      for (int c0 = 0; c0 < NT && c0 < g.T; c0 += 16) {
-        float v[16];
-        tc::ld16(tmem + (uint32_t)c0 + ((uint32_t)(32 * wq) << 16), v);
+  // Tensor memory is given back before the CTAs of a cluster wait for one
+  // another: a CTA of another kernel (or cluster) that waits for it on this SM
+  // may be the one that a holder elsewhere waits for.
+  float *part = reinterpret_cast<float *>(smem);   // [NT][128], in the memory of the stages
+  if (warp >= 2) {
+    for (int c0 = 0; c0 < NT && c0 < g.T; c0 += 16) {
+      float v[16];
+      tc::ld16(tmem + (uint32_t)c0 + ((uint32_t)(32 * wq) << 16), v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) put(c0 + j, v[j]);
+      for (int j = 0; j < 16; ++j) {
+        if (g.splits == 1) put(c0 + j, v[j]);
+        else part[(c0 + j) * 128 + 32 * wq + lane] = v[j];
       }
     }
-  } else {
-    // parts [NT][128] in the memory of the stages; rank r adds and writes tokens r, r + splits, ...
-    float *part = reinterpret_cast<float *>(smem);
-    if (warp >= 2) {
-      for (int c0 = 0; c0 < NT && c0 < g.T; c0 += 16) {
-        float v[16];
-        tc::ld16(tmem + (uint32_t)c0 + ((uint32_t)(32 * wq) << 16), v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c0 + j) * 128 + 32 * wq + lane] = v[j];
-      }
-    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after();
+    tc::dealloc(tmem, L::kCols);
+  }
+  if (g.splits > 1) {
     __syncwarp();
     tc::cluster_sync();
     if (warp >= 2) {
-      // four tokens' parts of up to 8 ranks in flight together, added in the order of the ranks
+      // rank r adds and writes tokens r, r + splits, ...: four tokens' parts of up to 8 ranks in flight
+      // together, added in the order of the ranks
       for (int64_t t0 = rank; t0 < g.T; t0 += 4 * g.splits) {
         float v[4][8];
 #pragma unroll
@@ -261,12 +264,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     }
     __syncwarp();
     tc::cluster_sync();   // no CTA leaves while its part is read
-  }
-  tc::fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc::fence_after();
-    tc::dealloc(tmem, L::kCols);
   }
   bad = __reduce_or_sync(0xffffffffu, bad);
   if (lane == 0) status_or(g.status, bad);
