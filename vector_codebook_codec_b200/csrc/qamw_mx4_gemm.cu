@@ -221,26 +221,31 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   // another: a CTA of another kernel (or cluster) that waits for it on this SM
   // may be the one that a holder elsewhere waits for.
   float *part = reinterpret_cast<float *>(smem);   // [NT][128], in the memory of the stages
-  if (warp >= 2) {
+  if (warp >= 2 && g.splits == 1) {
     for (int c0 = 0; c0 < NT && c0 < g.T; c0 += 16) {
       float v[16];
       tc::ld16(tmem + (uint32_t)c0 + ((uint32_t)(32 * wq) << 16), v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (g.splits == 1) put(c0 + j, v[j]);
-        else part[(c0 + j) * 128 + 32 * wq + lane] = v[j];
-      }
+      for (int j = 0; j < 16; ++j) put(c0 + j, v[j]);
+    }
+  } else if (warp >= 2) {
+    for (int c0 = 0; c0 < NT && c0 < g.T; c0 += 16) {
+      float v[16];
+      tc::ld16(tmem + (uint32_t)c0 + ((uint32_t)(32 * wq) << 16), v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) part[(c0 + j) * 128 + 32 * wq + lane] = v[j];
     }
   }
   tc::fence_before();
   __syncthreads();
+  if (g.splits > 1) tc::cluster_arrive();
   if (warp == 1) {
     tc::fence_after();
     tc::dealloc(tmem, L::kCols);
+    __syncwarp();
   }
   if (g.splits > 1) {
-    __syncwarp();
-    tc::cluster_sync();
+    tc::cluster_wait();
     if (warp >= 2) {
       // rank r adds and writes tokens r, r + splits, ...: four tokens' parts of up to 8 ranks in flight
       // together, added in the order of the ranks
