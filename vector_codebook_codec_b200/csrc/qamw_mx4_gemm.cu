@@ -222,12 +222,18 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   // may be the one that a holder elsewhere waits for.
   float *part = reinterpret_cast<float *>(smem);   // [NT][128], in the memory of the stages
   if (warp >= 2 && g.splits == 1) {
-    for (int c0 = 0; c0 < NT && c0 < g.T; c0 += 16) {
-      float v[16];
-      tc::ld16(tmem + (uint32_t)c0 + ((uint32_t)(32 * wq) << 16), v);
+    auto write = [&](auto *y, auto rounded) {       // one type for the whole tile
+      y += m;
+      for (int c0 = 0; c0 < NT && c0 < g.T; c0 += 16, y += 16 * g.ldy) {
+        float v[16];
+        tc::ld16(tmem + (uint32_t)c0 + ((uint32_t)(32 * wq) << 16), v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) put(c0 + j, v[j]);
-    }
+        for (int j = 0; j < 16; ++j)
+          if (m < g.M && c0 + j < g.T) y[j * g.ldy] = rounded(v[j]);
+      }
+    };
+    if (g.out_bf16) write(static_cast<__nv_bfloat16 *>(g.Y), [](float v) { return __float2bfloat16_rn(v); });
+    else write(static_cast<float *>(g.Y), [](float v) { return v; });
   } else if (warp >= 2) {
     for (int c0 = 0; c0 < NT && c0 < g.T; c0 += 16) {
       float v[16];
