@@ -12,7 +12,9 @@
 // its error, and both y - m and y + m are rounded to 4 bits. Where they agree,
 // so does every value between them, the exact one among them. Where they
 // differ (about 6 in 10^5 values of Gaussian rows at b = 128), or the group's
-// exponent hangs on the error, the warp forms the value in fp64 from the row.
+// exponent hangs on the error, or the group is so small beside its block that
+// m is not small beside its values (64 m above its largest), the warp forms the
+// values in fp64 from the row.
 // An e2m1 border has at most three significant bits, so the exponent and the
 // top mantissa bits of that double, with a sticky bit for the rest, decide
 // exactly (double_scaled).
@@ -429,7 +431,10 @@ __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxReside
           const float lo = fmaxf(t - m, 0.0f), hi = t + m;
           e[r] = (int)(__float_as_uint(lo) >> 23) - 127 - 2;
           const bool zero = Q == 0.0f || !in[r];
-          const bool sure = Q > 0x1p-100f && Q < 0x1p100f && (__float_as_uint(lo) >> 23) == (__float_as_uint(hi) >> 23);
+          // The third condition: a group that cancels to within some times m. It leaves 2 m 2^-e <= 1/4, so that
+          // y - m and y + m, where they differ in sign, both round to 0: |y +- m| is then at most 2 m.
+          const bool sure = Q > 0x1p-100f && Q < 0x1p100f && 64.0f * m <= lo &&
+                            (__float_as_uint(lo) >> 23) == (__float_as_uint(hi) >> 23);
           if (!sure) e[r] = -127;
           if (!sure && !zero) again[r] = 0xffffu;
           const float up = sure ? __uint_as_float((uint32_t)(127 - e[r]) << 23) : 0.0f;   // !sure: codes 0 for now
@@ -450,7 +455,7 @@ __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxReside
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t a = e2m1x8(u[r] + 8 * h), b = e2m1x8(v[r] + 8 * h);
-            c[r][h] = a & b;          // a value within m of zero differs in its sign alone: it is +0
+            c[r][h] = a & b;          // a difference in the sign alone: both are 0 (see `sure`), and so is the value
             d[r][h] = (a ^ b) & 0x77777777u;
             open |= d[r][h];
           }
