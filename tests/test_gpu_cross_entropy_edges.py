@@ -1,0 +1,90 @@
+"""The head's cross entropy and its gradient at the ends of what they take:
+tokens that the model is sure of, logits near the largest fp32 number, and the
+same call again.
+
+Logits here are products of one term, so they are exact. A loss is
+(max - l_target) + log(sum): the difference of two logits, rounded once
+(2^-24 of it), and the logarithm of a sum that starts at 1. Its error: two
+or three roundings of 2^-24 where the sum is near 1 (a warp's, and the tiles'),
+(12 + 4) 2^-24 + 12 x 1.3e-8 < 2^-19 of every other term (its argument's
+rounding, the exponential, and log2 e in fp32), a step of the logarithm:
+  |loss - loss64| <= 4 2^-24 + 2^-19 loss64."""
+import math
+
+import pytest
+import torch
+
+import vector_codebook_codec_b200 as qamw
+from test_gpu_cross_entropy import _case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(lib):
+    return lib
+
+
+@pytest.mark.parametrize("top", [15.0, 30.0, 100.0, 300.0, 4096.0, -300.0])
+@pytest.mark.parametrize("V", [2, 700, 5000])
+def test_loss_of_a_sure_token(top, V):
+    """A second logit 12 below the first: the loss of 6.1e-6 is far below a step of the normaliser."""
+    W = torch.full((V, 16), 0.0, dtype=torch.bfloat16)
+    X = torch.zeros((9, 16), dtype=torch.bfloat16)
+    X[:, 0] = 1
+    for t in torch.randint(0, V, (6,), generator=torch.Generator().manual_seed(V)).tolist():
+        W[:, 0] = top - 80
+        W[t, 0] = top
+        W[(t + 1) % V, 0] = top - 12
+        z = W[:, 0].double()
+        ref = torch.log1p(torch.exp(z - z[t]).sum() - 1).item()
+        loss, _ = qamw.cross_entropy(X.cuda(), W.cuda(), torch.full((9,), t, device="cuda"))
+        assert ref > 0 and ((loss.double() - ref).abs() <= 4 * 2.0 ** -24 + 2.0 ** -19 * ref).all(), (loss, ref)
+
+
+def _lowest_and_largest():
+    V, K, low = 600, 8, torch.finfo(torch.bfloat16).min
+    X = torch.zeros((4, K), dtype=torch.bfloat16)
+    W = torch.zeros((V, K), dtype=torch.bfloat16)
+    X[0, 0] = 1                      # every logit at the lowest value
+    W[:, 0] = low
+    X[1, 1] = 1                      # half of them, the others small
+    W[::2, 1] = low
+    W[1::2, 1] = torch.linspace(-2, 2, V // 2)
+    X[2, 2] = 1                      # one at the largest
+    W[:, 2] = 1
+    W[7, 2] = -low
+    X[3, 3] = 1                      # the lowest and the largest together
+    W[:, 3] = low
+    W[9, 3] = -low
+    t = torch.tensor([5, 11, 7, 9])
+    z = X.double() @ W.double().t()
+    return X.cuda(), W.cuda(), t.cuda(), z.cuda()
+
+
+def test_logits_near_the_largest_number():
+    """Entries masked with the type's lowest value, tokens for which nothing else is left, and a logit near the top."""
+    X, W, t, z = _lowest_and_largest()
+    loss, lse = qamw.cross_entropy(X, W, t)
+    lse64 = torch.logsumexp(z, dim=1)
+    assert ((lse.double() - lse64).abs() <= 2.0 ** -21 * (1 + lse64.abs())).all()
+    want = torch.tensor([math.log(W.shape[0]), (lse64[1] - z[1, 11]).item(), 0.0, 0.0], dtype=torch.float64, device="cuda")
+    assert ((loss.double() - want).abs() <= 2.0 ** -20 * (1 + want)).all()
+
+
+@pytest.mark.parametrize("T,V,K", [(1, 1000, 256), (16, 3001, 1024), (301, 5021, 512), (700, 9000, 1024)])
+def test_the_same_call_gives_the_same_bits(T, V, K):
+    """Alone, and with another batch's passes before and after that nothing waits for."""
+    X, W, t, g = _case(T, K, V, 70)
+    Y, _, u, h = _case(T, K, V, 71)
+    loss, lse = qamw.cross_entropy(X, W, t)
+    want = (loss, lse) + qamw.cross_entropy_grad(X, W, t, lse, g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for Z, v, w in ((X, t, g), (Y, u, h), (X, t, g)):
+            loss, l = qamw.cross_entropy(Z, W, v)
+            got.append((loss, l) + qamw.cross_entropy_grad(Z, W, v, l, w))
+        torch.cuda.synchronize()
+        for r in (got[0], got[2]):
+            assert all(torch.equal(a, b) for a, b in zip(r, want))

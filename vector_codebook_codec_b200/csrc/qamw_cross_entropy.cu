@@ -59,7 +59,7 @@ struct CeArgs {
   // kStats, kGrad: rows are tokens, columns the vocabulary entries v0 ..
   const int64_t *targets;         // [T]
   int64_t v0, V, ignore;
-  float2 *partials;               // kStats: [half tiles of the whole vocabulary][T] (max * log2 e, sum relative to it)
+  float2 *partials;               // kStats: [half tiles of the whole vocabulary][T] (maximum, sum relative to it)
   float *target_logit;            // kStats: [T]
   const float *lse, *grad;        // kGrad: [T]
   const float *factor;            // kGrad: of G (divided out); kStore: of D
@@ -134,7 +134,12 @@ __device__ __forceinline__ Unit unit_of(const CeArgs &g, int64_t u) {
   return r;
 }
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// log2 of exp(a) / exp(ref) and of exp(b) / exp(ref)
+__device__ __forceinline__ float2 log2_ratio(float a, float b, float ref) {
+  return mul2(add2(make_float2(a, b), make_float2(-ref, -ref)), make_float2(kLog2e, kLog2e));
+}
 
 // A_MN / B_MN: the operand lies [contraction][rows or columns] in memory.
 template <int CTAS, bool A_MN, bool B_MN, int EPI>
@@ -282,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       int tcol = -1;                       // the target's column among this warp's
-      float m = -INFINITY, sum = 0.0f;     // kStats
+      float m = -INFINITY;                 // kStats
+      float2 sum = make_float2(0.0f, 0.0f);   // of even and odd columns
       float lse2 = 0.0f, gr = 0.0f;        // kGrad
       if constexpr (EPI == kStats || EPI == kGrad) {
         const int64_t t = in ? g.targets[row] : g.ignore;
@@ -325,12 +331,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           float top = v[0];
 #pragma unroll
           for (int j = 1; j < 32; ++j) top = fmaxf(top, v[j]);
-          // the reference in units of log 2; a row of -Inf so far has none
-          const float mn = fmaxf(m, top * kLog2e), ref = mn == -INFINITY ? 0.0f : mn;
-          sum *= exp2f(m - ref);
+          // The difference of the logits comes first, then log2 e: neither rounds nor overflows with the logits'
+          // own size. A row of -Inf so far has no reference.
+          const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.0f : mn;
+          const float less = exp2f((m - ref) * kLog2e);
+          sum = mul2(sum, make_float2(less, less));
           m = mn;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sum += exp2f(__fmaf_rn(v[j], kLog2e, -ref));
+          for (int j = 0; j < 32; j += 2) {
+            const float2 d = log2_ratio(v[j], v[j + 1], ref);
+            sum = add2(sum, make_float2(exp2f(d.x), exp2f(d.y)));
+          }
         } else if constexpr (EPI == kGrad) {
           const bool none = gr == 0.0f;
 #pragma unroll
@@ -375,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if constexpr (EPI == kStats)
-        if (in && n_cols > 0) g.partials[((g.v0 + col0) / kHalf) * g.rows + row] = make_float2(m, sum);
+        if (in && n_cols > 0) g.partials[((g.v0 + col0) / kHalf) * g.rows + row] = make_float2(m, sum.x + sum.y);
       tc::fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -412,7 +423,7 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const float2 
   const int64_t t = (int64_t)blockIdx.x * 32 + lane;
   auto join = [](float2 a, float2 b) {
     const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.0f : m;
-    return make_float2(m, a.y * exp2f(a.x - ref) + b.y * exp2f(b.x - ref));
+    return make_float2(m, a.y * exp2f((a.x - ref) * kLog2e) + b.y * exp2f((b.x - ref) * kLog2e));
   };
   tc::griddep_launch_dependents();
   tc::griddep_wait();
@@ -423,8 +434,11 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const float2 
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         q[k] = i + 32 * k < n_tiles ? partials[(i + 32 * k) * T + t] : make_float2(-INFINITY, 0.0f);
+      const float m = fmaxf(fmaxf(p.x, fmaxf(q[0].x, q[1].x)), fmaxf(q[2].x, q[3].x)), ref = m == -INFINITY ? 0.0f : m;
+      float sum = p.y * exp2f((p.x - ref) * kLog2e);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) p = join(p, q[k]);
+      for (int k = 0; k < 4; ++k) sum += q[k].y * exp2f((q[k].x - ref) * kLog2e);
+      p = make_float2(m, sum);
     }
   }
   part[sl][lane] = p;
@@ -436,12 +450,13 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const float2 
     p = join(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o), __shfl_xor_sync(0xffffffffu, p.y, o)));
   const int64_t tt = (int64_t)blockIdx.x * 32 + sl;
   if (lane != 0 || tt >= T) return;
-  const float n = __fmaf_rn(p.x, kLn2, logf(p.y));
+  const float n = logf(p.y);
   const int64_t at = targets[tt];
   const bool real = at >= 0 && at < V;
   if (at != ignore && !real) status_or(status, QAMW_STATUS_BAD_INDEX);
-  lse[tt] = n;
-  loss[tt] = (at != ignore && real) ? n - target_logit[tt] : 0.0f;
+  lse[tt] = p.x + n;
+  // not lse - target: of a token that the model is sure of, the whole loss lies below a step of lse
+  loss[tt] = (at != ignore && real) ? (p.x - target_logit[tt]) + n : 0.0f;
 }
 
 // Before the backward pass. CTA 0: the factor of G, max |g| over the tokens that
