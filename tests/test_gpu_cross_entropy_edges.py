@@ -72,6 +72,18 @@ def test_logits_near_the_largest_number():
     assert ((loss.double() - want).abs() <= 2.0 ** -20 * (1 + want)).all()
 
 
+def test_gradient_of_logits_near_the_largest_number():
+    """exp(l - lse) of the same: the entries of G and dW stay finite (dX sums products beyond fp32)."""
+    X, W, t, z = _lowest_and_largest()
+    lse = torch.logsumexp(z, dim=1).float()
+    g = torch.tensor([1.0, 0.5, 0.25, 2.0], device="cuda")
+    _, dW = qamw.cross_entropy_grad(X, W, t, lse, g)
+    G = torch.exp(z - lse.double()[:, None])
+    G.scatter_add_(1, t[:, None], -torch.ones_like(z[:, :1]))
+    ref = (G * g.double()[:, None]).t() @ X.double()
+    assert ((dW.double() - ref).abs() <= 2.0 ** -7 * ref.abs() + 2.0 ** -22).all()
+
+
 @pytest.mark.parametrize("T,V,K", [(1, 1000, 256), (16, 3001, 1024), (301, 5021, 512), (700, 9000, 1024)])
 def test_the_same_call_gives_the_same_bits(T, V, K):
     """Alone, and with another batch's passes before and after that nothing waits for."""

@@ -289,14 +289,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tcol = -1;                       // the target's column among this warp's
       float m = -INFINITY;                 // kStats
       float2 sum = make_float2(0.0f, 0.0f);   // of even and odd columns
-      float lse2 = 0.0f, gr = 0.0f;        // kGrad
+      float lse = 0.0f, gr = 0.0f;         // kGrad
       if constexpr (EPI == kStats || EPI == kGrad) {
         const int64_t t = in ? g.targets[row] : g.ignore;
         const bool live = t != g.ignore && t >= 0 && t < g.V;
         const int64_t off = t - (g.v0 + col0);
         if (live && off >= 0 && off < n_cols) tcol = (int)off;
         if constexpr (EPI == kGrad) {
-          lse2 = in ? g.lse[row] * kLog2e : 0.0f;
+          lse = in ? g.lse[row] : 0.0f;
           gr = live ? __fdiv_rn(g.grad[row], *g.factor) : 0.0f;
         }
       }
@@ -345,10 +345,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if constexpr (EPI == kGrad) {
           const bool none = gr == 0.0f;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float p = exp2f(__fmaf_rn(v[j], kLog2e, -lse2));
-            if (j == tcol - c) p -= 1.0f;
-            v[j] = none ? 0.0f : gr * p;
+          for (int j = 0; j < 32; j += 2) {
+            const float2 d = log2_ratio(v[j], v[j + 1], lse);
+            float p[2] = {exp2f(d.x), exp2f(d.y)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (j + i == tcol - c) p[i] -= 1.0f;
+              v[j + i] = none ? 0.0f : gr * p[i];
+            }
           }
         }
         if constexpr (EPI == kStore) {
