@@ -1,6 +1,6 @@
 """The head's cross entropy and its gradient at the ends of what they take:
-tokens that the model is sure of, logits near the largest fp32 number, and the
-same call again.
+tokens that the model is sure of, logits near the largest fp32 number, targets
+out of range, and the same call again.
 
 Logits here are products of one term, so they are exact. A loss is
 (max - l_target) + log(sum): the difference of two logits, rounded once
@@ -15,7 +15,7 @@ import pytest
 import torch
 
 import vector_codebook_codec_b200 as qamw
-from test_gpu_cross_entropy import _case
+from test_gpu_cross_entropy import _case, _coded_heads
 
 pytestmark = pytest.mark.gpu
 
@@ -82,6 +82,31 @@ def test_gradient_of_logits_near_the_largest_number():
     G.scatter_add_(1, t[:, None], -torch.ones_like(z[:, :1]))
     ref = (G * g.double()[:, None]).t() @ X.double()
     assert ((dW.double() - ref).abs() <= 2.0 ** -7 * ref.abs() + 2.0 ** -22).all()
+
+
+def test_gradient_reports_targets_out_of_range():
+    """qamw.h: another target outside [0, V) is left out and sets the status, in the gradient's calls too."""
+    X, W, t, g = _case(40, 64, 500, 13, ignored=0.0)
+    _, lse = qamw.cross_entropy(X, W, t)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qamw.cross_entropy_grad(X, W, t, lse, g, status=status)
+    assert status.item() == 0
+    for bad in (500, -1, 2 ** 40):
+        for piece in (None, 256):
+            u = t.clone()
+            u[39] = bad
+            status.zero_()
+            qamw.cross_entropy_grad(X, W, u, lse, g, piece=piece, status=status)
+            assert status.item() == qamw.STATUS_BAD_INDEX
+    enc, C, mx = _coded_heads(500, 64 * 2, 5)
+    X, _, t, g = _case(40, 128, 500, 14, ignored=0.5)
+    _, lse = qamw.cross_entropy(X, mx, t)
+    status.zero_()
+    qamw.cross_entropy_grad(X, mx, t, lse, g, piece=256, status=status)
+    assert status.item() == 0
+    t[3] = 501
+    qamw.cross_entropy_grad(X, mx, t, lse, g, piece=256, status=status)
+    assert status.item() == qamw.STATUS_BAD_INDEX
 
 
 @pytest.mark.parametrize("T,V,K", [(1, 1000, 256), (16, 3001, 1024), (301, 5021, 512), (700, 9000, 1024)])

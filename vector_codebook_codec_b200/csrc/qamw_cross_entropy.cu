@@ -464,12 +464,13 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const float2 
 }
 
 // Before the backward pass. CTA 0: the factor of G, max |g| over the tokens that
-// count (1 if that is 0, Inf or NaN). The others: X with the rows of ignored
+// count (1 if that is 0, Inf or NaN), and the report of targets out of range. The others: X with the rows of ignored
 // tokens set to zero, [T][K], eight columns a thread: their G is zero, but dW =
 // G^T X would still turn an Inf or NaN of a padded row into NaN.
 __global__ void __launch_bounds__(256) ce_prepare_kernel(const uint4 *X, int64_t ldx8, const int64_t *targets,
                                                          const float *grad, int64_t T, int64_t K8, int64_t V,
-                                                         int64_t ignore, uint4 *live, float *factor) {
+                                                         int64_t ignore, uint4 *live, float *factor,
+                                                         int32_t *status) {
   tc::griddep_launch_dependents();
   auto counts = [&](int64_t t) {
     const int64_t at = targets[t];
@@ -478,8 +479,12 @@ __global__ void __launch_bounds__(256) ce_prepare_kernel(const uint4 *X, int64_t
   if (blockIdx.x == 0) {
     __shared__ uint32_t part[8];
     uint32_t top = 0;   // magnitudes as integers: ordered alike, NaN the largest
-    for (int64_t t = threadIdx.x; t < T; t += 256)
+    bool bad = false;
+    for (int64_t t = threadIdx.x; t < T; t += 256) {
       if (counts(t)) top = max(top, __float_as_uint(grad[t]) & 0x7FFFFFFFu);
+      else bad |= targets[t] != ignore;
+    }
+    if (bad) status_or(status, QAMW_STATUS_BAD_INDEX);
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
     __syncthreads();
@@ -690,7 +695,8 @@ cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const floa
   if (first) {
     const int64_t blocks = (a.T * a.K / 8 + 255) / 256, most = (int64_t)sm_count() * 16;
     ce_prepare_kernel<<<(unsigned)(1 + std::min(blocks, most)), 256, 0, s>>>(
-        static_cast<const uint4 *>(a.X), a.ldx / 8, a.targets, grad, a.T, a.K / 8, a.V, a.ignore, live, factor);
+        static_cast<const uint4 *>(a.X), a.ldx / 8, a.targets, grad, a.T, a.K / 8, a.V, a.ignore, live, factor,
+        a.status);
     const cudaError_t c = cudaGetLastError();
     if (c != cudaSuccess) return c;
   }
