@@ -412,7 +412,9 @@ int qamw_mx4_quantize(const void *W, qamw_dtype w_dtype, int64_t M, int64_t K, i
  * qamw_mx4_decode -- the coded matrix in its original basis,
  *   w_hat_j = d_j (H_b (q 2^e))_j / sqrt(b), divided by s_j (times s_j if divide != 0),
  * fp32 arithmetic, rounded (RNE) to out_dtype. With block == 0 and col_scale
- * == NULL it writes the values q 2^e themselves, exact in both types.
+ * == NULL it writes the values q 2^e themselves, exact in both types. Rows with
+ * a scale byte of 240 or more, and columns whose 1 / (sqrt(b) s_j) is no normal
+ * fp32 number (with them the others of their 1024), are formed in fp64.
  * Arguments as given to the quantisation; W_out: device [M][ldo].
  */
 int qamw_mx4_decode(const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K, const float *col_scale,

@@ -1,15 +1,21 @@
 """The microscaled 4-bit operators where they can go wrong at the ends of what
-they take: groups that cancel against the rest of their block.
+they take: groups that cancel against the rest of their block, and the largest and
+smallest scales of a decode.
 
 Quantisation: the inputs are multiples of 2^-24 below 2^20, so a block's sums
-are exact in fp64 in any order, and the codes have to be the oracle's."""
+are exact in fp64 in any order, and the codes have to be the oracle's.
+
+Decode, as in test_gpu_mx4.py, with A = sum_block |q 2^e| / sqrt(b) / s:
+  |x - x_ref| <= (log2 b + 4) 2^-24 A, plus half a step of the subnormal
+numbers (2^-150) for fp32; for bf16 2^-8 |x_ref| and 2^-134 more. What the type
+cannot hold (above its largest value by more than half a step) is Inf."""
 import numpy as np
 import pytest
 import torch
 
 import vector_codebook_codec_b200 as qamw
-from oracle import codec
-from test_gpu_mx4 import _check_quantized
+from oracle import codec, mx4
+from test_gpu_mx4 import _check_quantized, _scale
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +67,98 @@ def test_quantize_equal_outliers(block, apart, dtype):
         sd = None if s is None else torch.from_numpy(s).cuda()
         q = qamw.mx4_quantize(t.cuda(), block, block + apart, sd, divide=divide)
         _check_quantized(q, W, s, divide, block, block + apart)
+
+
+def _check_decoded(q, dtype, code, byte, s, divide, block, seed):
+    M, K = code.shape
+    got = qamw.mx4_decode(q, dtype).double().cpu().numpy()
+    with np.errstate(all="ignore"):
+        ref = mx4.decode(code, byte, s, divide, block, seed)
+        A = np.abs(mx4.values(code, byte))
+        if block:
+            A = np.repeat(A.reshape(M, K // block, block).sum(axis=2), block, axis=1) / np.sqrt(block)
+        if s is not None:
+            A = A * np.abs(s.astype(np.float64)) if divide else A / np.abs(s.astype(np.float64))
+        tol = (np.log2(max(block, 1)) + 4) * 2.0 ** -24 * A + 2.0 ** -150
+        if dtype == torch.bfloat16:
+            tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref) + 2.0 ** -134
+        top = torch.finfo(dtype).max * (1 + torch.finfo(dtype).eps / 4)       # half a step above the largest value
+        held, over = np.abs(ref) + tol < top, np.abs(ref) - tol > top
+        assert (np.abs(got - ref) <= tol)[held].all()
+        assert (got == np.sign(ref) * np.inf)[over].all()
+        assert np.array_equal(np.isnan(got), np.isnan(ref))
+    return held
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", [0, 16, 32, 64, 256, 1024])
+@pytest.mark.parametrize("power", [124, 100, -100, -126, -145])
+def test_decode_magnitudes_near_the_ends_of_fp32(power, block, dtype):
+    """Rows of 2^power, which the quantisation takes, come back: no Inf or 0 before the last rounding."""
+    M, K = 140, 2048
+    g = np.random.default_rng(block + power + 200)
+    t = torch.from_numpy((np.clip(g.standard_normal((M, K)), -3, 3) * 2.0 ** power).astype(np.float32))
+    for s, divide in ((None, False), (_scale(K, 9), False), (_scale(K, 9), True)):
+        q = qamw.mx4_quantize(t.cuda(), block, 3, None if s is None else torch.from_numpy(s).cuda(), divide=divide)
+        code, byte = mx4.unpack_codes(q.codes.cpu().numpy()), qamw.mx4_scale_rows(q).cpu().numpy()
+        held = _check_decoded(q, dtype, code, byte, s, divide, block, 3)
+        assert held.mean() > 0.9
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", [0, 2, 32, 64, 128, 512, 1024])
+def test_decode_any_scale_byte(block, dtype):
+    """Scale bytes of the whole range beside one another, NaN and empty groups among them."""
+    M, K = 90, 1056 if block <= 32 else 2048
+    g = np.random.default_rng(block)
+    byte = g.integers(0, 255, (M, K // 32)).astype(np.uint8)
+    byte[:30] = g.integers(90, 160, (30, K // 32))
+    byte[5, 3], byte[40, 7] = 255, 255
+    codes = g.integers(0, 256, (M, K // 2)).astype(np.uint8)
+    codes[20:25, 16:64] = 0
+    byte[20:25, 1:4] = 0
+    code = mx4.unpack_codes(codes)
+    for s, divide in ((None, False), (_scale(K, 1), False), (_scale(K, 1), True)):
+        q = qamw.mx4_from_parts(torch.from_numpy(codes).cuda(), torch.from_numpy(byte).cuda(), block, 11,
+                                None if s is None else torch.from_numpy(s).cuda(), divide)
+        _check_decoded(q, dtype, code, byte, s, divide, block, 11)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", [0, 32, 256])
+@pytest.mark.parametrize("value", [2.0 ** -149, 2.0 ** -140, 2.0 ** -126, 2.0 ** 126, -2.0 ** 127])
+def test_decode_extreme_column_scales(value, block, dtype):
+    """Columns whose s lies at the ends of fp32, 1/s beyond them: x / s and x s as they are defined."""
+    M, K = 70, 1024
+    g = np.random.default_rng(block + 1)
+    codes = g.integers(0, 256, (M, K // 2)).astype(np.uint8)
+    byte = g.integers(60, 200, (M, 1)).astype(np.uint8).repeat(K // 32, axis=1)
+    s = _scale(K, 2)
+    s[40:44], s[700] = value, value
+    code = mx4.unpack_codes(codes)
+    for divide in (False, True):
+        q = qamw.mx4_from_parts(torch.from_numpy(codes).cuda(), torch.from_numpy(byte).cuda(), block, 4,
+                                torch.from_numpy(s).cuda(), divide)
+        _check_decoded(q, dtype, code, byte, s, divide, block, 4)
+
+
+@pytest.mark.parametrize("value", [0.0, float("inf"), float("nan")])
+def test_decode_zero_and_infinite_column_scales(value):
+    """x / 0, x / Inf, 0 Inf and their like (sums inside a group of 32 are exact, so a zero is one)."""
+    M, K = 20, 256
+    g = np.random.default_rng(3)
+    codes = g.integers(0, 256, (M, K // 2)).astype(np.uint8)
+    byte = g.integers(100, 150, (M, K // 32)).astype(np.uint8)
+    s = _scale(K, 2)
+    s[40:44] = value
+    code = mx4.unpack_codes(codes)
+    for block in (0, 32):
+        for divide in (False, True):
+            q = qamw.mx4_from_parts(torch.from_numpy(codes).cuda(), torch.from_numpy(byte).cuda(), block, 4,
+                                    torch.from_numpy(s).cuda(), divide)
+            got = qamw.mx4_decode(q, torch.float32).cpu().numpy()
+            with np.errstate(all="ignore"):
+                ref = mx4.decode(code, byte, s, divide, block, 4)
+            odd = ~np.isfinite(ref)
+            assert np.array_equal(got[odd], ref[odd].astype(np.float32), equal_nan=True)
+            assert (got[:, 40:44][~odd[:, 40:44]] == 0).all() and np.isfinite(got[~odd]).all()

@@ -571,6 +571,45 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *p, int vec, const float (
   }
 }
 
+// Scale bytes from which the decode's fp32 sums (of up to 32 groups, each up to
+// 32 x 6 x 2^e) may overflow: e > 112. Small ones lose nothing: the sums are
+// multiples of 2^-128, which fp32 holds down to its subnormal numbers.
+constexpr uint32_t kBeyondFp32 = 240;
+
+// The rows of a warp that have such a byte (found by one more pass over their
+// scales), or all of them if a column's factor is no normal number, from the
+// definition, in fp64 and rounded once: a value may be within the type although
+// the sum before its division by sqrt(b) s is not, or the other way round.
+template <typename T>
+__device__ __noinline__ void decode_exactly(const MxDecodeArgs &p, bool every) {
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = blockIdx.x % p.units_k, first = (blockIdx.x / p.units_k) * kMxWarps + (threadIdx.x >> 5);
+  const int64_t k_tiles = (p.K + 127) / 128, run0 = LanePlace(unit, lane).run0, b = (int64_t)1 << p.log2b;
+  const int64_t end = min((unit + 1) * kMxUnit, p.K);
+  __syncwarp();                       // the lanes' stores of the pass before come first
+  for (int64_t row = first; row < p.M; row += p.row_groups) {
+    const uint8_t *codes = p.codes + row * (p.K / 2);
+    bool beyond = every;
+    for (int64_t c = run0; c < run0 + 128 && c < p.K; c += 64)
+      beyond |= p.scales[scale_offset(row, c / 32, k_tiles)] >= kBeyondFp32;
+    if (!__any_sync(0xffffffffu, beyond)) continue;
+    for (int64_t col = unit * kMxUnit + lane; col < end; col += 32) {
+      double x = 0.0;
+      for (int64_t c = col & ~(b - 1), last = c + b; c < last; ++c) {
+        const uint32_t byte = p.scales[scale_offset(row, c / 32, k_tiles)], q = codes[c / 2] >> (4 * (c & 1));
+        double v = (double)((0xC8643210u >> (4 * (q & 7u))) & 15u);               // twice the element
+        v *= byte == 255u ? nan("") : __hiloint2double((int)(byte + 895u) << 20, 0);   // 2^(byte - 128)
+        x += ((q >> 3) ^ __popcll(c & col & (b - 1))) & 1 ? -v : v;
+      }
+      if (p.log2b > 0) x *= (mask_is_negative(p.seed, col) ? -1.0 : 1.0) / sqrt((double)b);
+      if (p.s != nullptr) x = p.divide ? x * (double)p.s[col] : x / (double)p.s[col];
+      T *o = static_cast<T *>(p.out) + row * p.ldo + col;
+      if constexpr (sizeof(T) == 2) *o = __double2bfloat16(x);
+      else *o = (float)x;
+    }
+  }
+}
+
 // x = d (.) (H_b q 2^e) / (sqrt(b) s) (times s for divided rows): one rounding
 // to the output type at the end, like the codec's own decode; without a
 // rotation and a scale every value is exact in either type. Lanes hold what
@@ -601,9 +640,11 @@ __global__ void __launch_bounds__(32 * kMxWarps, (LB > 0 ? kMxResident : kMxResi
   if (rg < p.M) fetch(rg);
   const float inv = (float)(1.0 / sqrt((double)(1 << LB)));
   __shared__ Factors shared;
+  bool odd = false;                   // a factor that is no normal number
   form_factors(shared, unit, p.K, [&](int64_t col) {
     float v = inv;
     if (p.s != nullptr) v = p.divide ? __fmul_rn(inv, p.s[col]) : __fdiv_rn(inv, p.s[col]);
+    odd |= !(fabsf(v) >= 0x1p-126f && fabsf(v) < INFINITY);
     return (LB > 0 && mask_is_negative(p.seed, col)) ? -v : v;
   });
   float2 f[LB > 0 ? 16 : 1];          // in registers where the exchanges keep the L1 pipe busy
@@ -611,6 +652,7 @@ __global__ void __launch_bounds__(32 * kMxWarps, (LB > 0 ? kMxResident : kMxResi
 #pragma unroll
     for (int j = 0; j < 16; ++j) f[j] = factor(shared, lane, j);
   }
+  uint32_t top = __syncthreads_or(odd) ? 256u : 0u;   // the largest scale byte, or 256
   for (int64_t row = rg; row < p.M; row += p.row_groups) {
     __half2 h[16];                    // (run 0, run 1) of column j
     {
@@ -627,7 +669,9 @@ __global__ void __launch_bounds__(32 * kMxWarps, (LB > 0 ? kMxResident : kMxResi
       }
     }
     const uint32_t sh = 4 * (lane & 2);
-    const float2 g = make_float2(e8m0_value((sw >> sh) & 255u), e8m0_value((sw >> (16 + sh)) & 255u));
+    const uint32_t b0 = (sw >> sh) & 255u, b1 = (sw >> (16 + sh)) & 255u;
+    const float2 g = make_float2(e8m0_value(b0), e8m0_value(b1));
+    top = max(top, max(b0, b1));
     if (row + p.row_groups < p.M) fetch(row + p.row_groups);
 #pragma unroll
     for (int t = 0; t < (LB < 4 ? LB : 4); ++t) {
@@ -663,6 +707,8 @@ __global__ void __launch_bounds__(32 * kMxWarps, (LB > 0 ? kMxResident : kMxResi
     if (in0) store16(o, p.vec, u);
     if (in1) store16(o + 64, p.vec, v);
   }
+  // without a rotation and a scale the values are exact for every byte
+  if ((LB > 0 || p.s != nullptr) && __any_sync(0xffffffffu, top >= kBeyondFp32)) decode_exactly<T>(p, top == 256u);
 }
 
 // One scale byte per (row, group), row-major, into the tiled layout (or back);
