@@ -1,6 +1,6 @@
 """The microscaled 4-bit operators where they can go wrong at the ends of what
-they take: groups that cancel against the rest of their block, and the largest and
-smallest scales of a decode.
+they take: groups that cancel against the rest of their block, the largest and
+smallest scales of a decode, a quantisation that takes long.
 
 Quantisation: the inputs are multiples of 2^-24 below 2^20, so a block's sums
 are exact in fp64 in any order, and the codes have to be the oracle's.
@@ -162,3 +162,19 @@ def test_decode_zero_and_infinite_column_scales(value):
             odd = ~np.isfinite(ref)
             assert np.array_equal(got[odd], ref[odd].astype(np.float32), equal_nan=True)
             assert (got[:, 40:44][~odd[:, 40:44]] == 0).all() and np.isfinite(got[~odd]).all()
+
+
+@pytest.mark.parametrize("T", [3, 100, 3000])
+def test_linear_with_a_slow_quantisation(T):
+    """Rows that rotate to one coefficient: all other groups are decided in fp64, some hundred times the usual
+    work, and the product that has been launched beside it waits."""
+    M, K, block = 200, 16384, 1024
+    g = np.random.default_rng(T)
+    X = codec.sign_mask(8, K) * torch.from_numpy(g.standard_normal((T, 1))).to(torch.bfloat16).double().numpy()
+    t = torch.from_numpy(X).to(torch.bfloat16).cuda()
+    W = qamw.mx4_quantize(torch.from_numpy(g.standard_normal((M, K)).astype(np.float32)).cuda(), block, 8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    Y = qamw.mx4_linear(W, t, status=status)
+    Xq = qamw.mx4_quantize(t, block, 8, divide=True)
+    assert torch.equal(Y, qamw.mx4_matmul(W, Xq)) and status.item() == 0
+    assert (qamw.mx4_scale_rows(Xq).view(T, K // block, block // 32)[:, :, 1:] == 0).all()

@@ -164,6 +164,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   tc::fence_after();
   const uint32_t tmem = tmem_slot;
   uint32_t bad = 0;
+  // by every thread, before any role's bounded waits begin: they then cover this kernel's own time only
+  if (g.after_quantize) tc::griddep_wait();
 
   if (warp == 0) {
     auto load_x = [&](int k, uint32_t s) {
@@ -173,7 +175,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
                       &full[s]);
       }
     };
-    if (g.after_quantize) tc::griddep_wait();
     for (int i = 0; i < early; ++i) load_x(k0 + i, i);
     int it = early;
     for (tc::Ring r; it < n; ++it, r.next(S)) {
@@ -324,9 +325,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int64_t n_tiles = g.walk.n_r * g.walk.n_c, step = gridDim.x / 2, first = blockIdx.x / 2;
   const int n_k = (int)((g.K + kBK - 1) / kBK);
   uint32_t bad = 0;
+  if (g.after_quantize) tc::griddep_wait();   // by every thread, before any role's bounded waits begin
 
   if (warp == 0) {
-    if (g.after_quantize) tc::griddep_wait();
     uint32_t it = 0;
     tc::Ring r;
     bool ok = true;
