@@ -1,0 +1,44 @@
+"""Calls of the 4-bit and cross-entropy operators that are refused before anything reaches the GPU: no GPU needed."""
+import pytest
+import torch
+
+import vector_codebook_codec_b200 as qamw
+
+
+@pytest.fixture
+def _host_tensors(lib, monkeypatch):
+    """The checks of type and shape alone, so that tensors in host memory pass for device ones."""
+    def need(name, t, dtype=None, ndim=None):
+        if t is not None and ((dtype is not None and t.dtype != dtype) or (ndim is not None and t.dim() != ndim)):
+            raise ValueError(name)
+    monkeypatch.setattr(qamw, "_need_cuda", need)
+
+
+def _encoded(V=512, K=256, bits=8):
+    return qamw.Encoded(torch.zeros((V, qamw.words_per_row(K, bits)), dtype=torch.int32), torch.ones(V), torch.ones(K),
+                        torch.ones(K // 2), V, K, 128, 1, 256, bits)
+
+
+def test_encoded_head_is_taken(_host_tensors):
+    h = qamw._Head(_encoded(), torch.zeros((256, 2)))
+    assert (h.V, h.K, h.ld) == (512, 256, 256)
+
+
+@pytest.mark.parametrize("field,value", [
+    ("row_norm", torch.ones(1024)[::2]), ("row_norm", torch.ones(1).expand(512)), ("row_norm", torch.ones(511)),
+    ("sigma", torch.ones(256)[::2]), ("sigma", torch.ones(1).expand(128)), ("sigma", torch.ones(256)),
+    ("col_scale", torch.ones(512)[::2]), ("col_scale", torch.ones(1).expand(256)),
+    ("packed", torch.zeros((512, 64), dtype=torch.int32)[:, :32]), ("packed", torch.zeros((1, 64), dtype=torch.int32).expand(512, 64)),
+])
+def test_encoded_head_with_a_strided_or_broadcast_part(_host_tensors, field, value):
+    """The decode takes every part as contiguous: a view with another stride would be read past its end."""
+    head = _encoded()
+    setattr(head, field, value)
+    with pytest.raises(ValueError):
+        qamw._Head(head, torch.zeros((256, 2)))
+
+
+@pytest.mark.parametrize("codebook", [torch.zeros((256, 1)), torch.zeros((256, 3)), torch.zeros((1, 512)), None])
+def test_encoded_head_with_another_codebook_shape(_host_tensors, codebook):
+    with pytest.raises(ValueError):
+        qamw._Head(_encoded(), codebook)

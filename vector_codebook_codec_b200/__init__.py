@@ -810,16 +810,15 @@ class _Head:
             if codebook is None:
                 raise ValueError("an Encoded head needs its codebook")
             _need_cuda("codebook", codebook, torch.float32, 2)
+            if codebook.shape[1] != 2:
+                raise ValueError("codebook must be [N, 2]")
             _need_cuda("head.packed", head.packed, torch.int32, 2)
             self.device = head.packed.device
-            _same_device(self.device, codebook=codebook, row_norm=head.row_norm, sigma=head.sigma,
-                         col_scale=head.col_scale)
+            _same_device(self.device, codebook=codebook, col_scale=head.col_scale)
             if head.packed.shape != (head.M, words_per_row(head.K, head.bits)) or not head.packed.is_contiguous():
                 raise ValueError("head.packed must be contiguous [M, words_per_row(K, bits)]")
-            _need_cuda("head.row_norm", head.row_norm, torch.float32, 1)
-            _need_cuda("head.sigma", head.sigma, torch.float32, 1)
-            if head.row_norm.shape[0] != head.M or head.sigma.shape[0] != head.K // 2:
-                raise ValueError("head.row_norm and head.sigma must be [M] and [K/2]")
+            _need_rows("head.row_norm", head.row_norm, head.M, self.device)
+            _need_rows("head.sigma", head.sigma, head.K // 2, self.device)
             _need_scale(self.device, head.col_scale, head.K)
 
     def rows(self, v0: int, n: int, status):
