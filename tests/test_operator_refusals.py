@@ -1,4 +1,6 @@
 """Calls of the 4-bit and cross-entropy operators that are refused before anything reaches the GPU: no GPU needed."""
+import types
+
 import pytest
 import torch
 
@@ -42,3 +44,9 @@ def test_encoded_head_with_a_strided_or_broadcast_part(_host_tensors, field, val
 def test_encoded_head_with_another_codebook_shape(_host_tensors, codebook):
     with pytest.raises(ValueError):
         qamw._Head(_encoded(), codebook)
+
+
+def test_stream_of_another_device():
+    """It would be passed over: the work would go to the current stream of the tensors' device."""
+    with pytest.raises(ValueError):
+        qamw._on(torch.device("cuda", 0), types.SimpleNamespace(device=torch.device("cuda", 1)))

@@ -551,6 +551,8 @@ def _switched(device, stream):
 def _on(device, stream):
     """``device`` as the current one and ``stream`` as its current stream, so
     that what a call allocates for itself belongs to the stream that uses it."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
     if stream is None and device.index == _torch()._C._cuda_getDevice():
         return _NULL_CONTEXT
     return _switched(device, stream)
