@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import vector_codebook_codec_b200 as qamw
+from test_abi_host import (ODD, QAMW_EINVAL, _cef, _ceg, _cew, _cgw, _mxd, _mxl, _mxq)
 
 
 @pytest.fixture
@@ -50,3 +51,12 @@ def test_stream_of_another_device():
     """It would be passed over: the work would go to the current stream of the tensors' device."""
     with pytest.raises(ValueError):
         qamw._on(torch.device("cuda", 0), types.SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+@pytest.mark.parametrize("call,argument", [(_mxq, "s"), (_mxd, "s"), (_mxl, "s"), (_cew, "loss"), (_cew, "lse"),
+                                           (_cef, "loss"), (_cef, "lse"), (_cef, "t"), (_cgw, "lse"), (_cgw, "g"),
+                                           (_ceg, "lse"), (_ceg, "g")])
+def test_misaligned_vectors(lib, call, argument):
+    """A float or int64 vector off its element's alignment would be a misaligned access on the GPU."""
+    assert call(lib, **{argument: ODD}) == QAMW_EINVAL
+    assert lib.qamw_last_error()

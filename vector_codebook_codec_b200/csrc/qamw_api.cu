@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -650,6 +651,14 @@ static bool element_aligned(const void *p, qamw_dtype t) {
   return reinterpret_cast<uintptr_t>(p) % (t == QAMW_BF16 ? 2 : 4) == 0;
 }
 
+// The float (or wider) vectors of an entry point lie at multiples of their element size.
+static int check_vectors(std::initializer_list<const void *> vectors, size_t element, const char *fn) {
+  for (const void *v : vectors)
+    if (reinterpret_cast<uintptr_t>(v) % element)
+      return fail(QAMW_EINVAL, "%s: a vector of %zu-byte elements is not aligned to them", fn, element);
+  return QAMW_OK;
+}
+
 size_t qamw_mx4_scale_bytes(int64_t M, int64_t K) {
   if (M < 1 || K < QAMW_MX4_GROUP || K % QAMW_MX4_GROUP || M > (int64_t(1) << 30) || K > (int64_t(1) << 24)) return 0;
   return mx4_scale_bytes(M, K);
@@ -669,6 +678,7 @@ int qamw_mx4_quantize(const void *W, qamw_dtype w_dtype, int64_t M, int64_t K, i
   if ((rc = check_mx4_codes(codes_out, scales_out, fn))) return rc;
   if (ldw < K) return fail(QAMW_EINVAL, "%s: ldw (%lld) < K (%lld)", fn, (long long)ldw, (long long)K);
   if (!element_aligned(W, w_dtype)) return fail(QAMW_EINVAL, "%s: W must be aligned to its element size", fn);
+  if ((rc = check_vectors({col_scale}, 4, fn))) return rc;
   Mx4QuantizeArgs a{W, w_dtype, M, K, ldw, col_scale, divide, block ? log2i(block) : 0, sign_seed, codes_out,
                     scales_out, status};
   cudaError_t e = launch_mx4_quantize(a, (cudaStream_t)stream);
@@ -689,6 +699,7 @@ int qamw_mx4_decode(const uint8_t *codes, const uint8_t *scales, int64_t M, int6
   if ((rc = check_mx4_codes(codes, scales, fn))) return rc;
   if (ldo < K) return fail(QAMW_EINVAL, "%s: ldo (%lld) < K (%lld)", fn, (long long)ldo, (long long)K);
   if (!element_aligned(W_out, out_dtype)) return fail(QAMW_EINVAL, "%s: W_out must be aligned to its element size", fn);
+  if ((rc = check_vectors({col_scale}, 4, fn))) return rc;
   Mx4DecodeArgs a{codes, scales, M, K, col_scale, divide, block ? log2i(block) : 0, sign_seed, W_out, out_dtype, ldo};
   cudaError_t e = launch_mx4_decode(a, (cudaStream_t)stream);
   return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
@@ -757,6 +768,7 @@ int qamw_mx4_linear(const uint8_t *w_codes, const uint8_t *w_scales, int64_t M, 
     return fail(QAMW_EINVAL, "%s: ldx (%lld) must be >= K and ldy (%lld) >= M", fn, (long long)ldx, (long long)ldy);
   if (!element_aligned(X, x_dtype) || !element_aligned(Y, out_dtype))
     return fail(QAMW_EINVAL, "%s: X and Y must be aligned to their element sizes", fn);
+  if ((rc = check_vectors({col_scale}, 4, fn))) return rc;
   const size_t need = qamw_mx4_linear_workspace_bytes(T, K);
   if (workspace == nullptr || workspace_bytes < need)
     return fail(QAMW_EWORKSPACE, "%s: workspace of %zu bytes needed (got %zu)", fn, need, workspace_bytes);
@@ -795,8 +807,7 @@ static int check_ce_piece(const CeArgsIn &a, const char *fn) {
                 (long long)a.ldw);
   if (reinterpret_cast<uintptr_t>(a.X) % 16 || reinterpret_cast<uintptr_t>(a.W) % 16)
     return fail(QAMW_EINVAL, "%s: X and W must be 16-byte aligned", fn);
-  if (reinterpret_cast<uintptr_t>(a.targets) % 8) return fail(QAMW_EINVAL, "%s: targets must be 8-byte aligned", fn);
-  return QAMW_OK;
+  return check_vectors({a.targets}, 8, fn);
 }
 
 static int check_ce_workspace(const void *workspace, size_t bytes, size_t need, const char *fn) {
@@ -834,6 +845,7 @@ int qamw_cross_entropy_finish(int64_t T, int64_t V, const int64_t *targets, int6
   int rc;
   if (!targets || !loss || !lse) return fail(QAMW_ENULL, "%s: targets, loss and lse must be non-NULL", fn);
   if ((rc = check_ce_sizes(T, 8, V, fn))) return rc;
+  if ((rc = check_vectors({loss, lse}, 4, fn)) || (rc = check_vectors({targets}, 8, fn))) return rc;
   if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_workspace(T, V).total, fn))) return rc;
   CeArgsIn a{nullptr, T, 8, 8, nullptr, V, 8, 0, V, targets, ignore_index, status};
   cudaError_t e = launch_ce_finish(a, workspace, loss, lse, (cudaStream_t)stream);
@@ -858,7 +870,7 @@ int qamw_cross_entropy_grad_piece(const void *X, int64_t T, int64_t K, int64_t l
   int rc;
   CeArgsIn a{X, T, K, ldx, W, n, ldw, v0, V, targets, ignore_index, status};
   if (!lse || !grad_loss) return fail(QAMW_ENULL, "%s: lse and grad_loss must be non-NULL", fn);
-  if ((rc = check_ce_piece(a, fn))) return rc;
+  if ((rc = check_ce_piece(a, fn)) || (rc = check_vectors({lse, grad_loss}, 4, fn))) return rc;
   if (piece < n || piece > (int64_t(1) << 30))
     return fail(QAMW_EINVAL, "%s: piece (%lld) must be at least n (%lld)", fn, (long long)piece, (long long)n);
   if (dW != nullptr && (lddw < K || reinterpret_cast<uintptr_t>(dW) % 2))
@@ -893,7 +905,7 @@ int qamw_cross_entropy(const void *X, int64_t T, int64_t K, int64_t ldx, const v
   int rc;
   if (!loss || !lse) return fail(QAMW_ENULL, "%s: loss and lse must be non-NULL", fn);
   CeArgsIn a{X, T, K, ldx, W, V, ldw, 0, V, targets, ignore_index, status};
-  if ((rc = check_ce_piece(a, fn))) return rc;
+  if ((rc = check_ce_piece(a, fn)) || (rc = check_vectors({loss, lse}, 4, fn))) return rc;
   if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_workspace(T, V).total, fn))) return rc;
   cudaError_t e = launch_ce_piece(a, workspace, (cudaStream_t)stream);
   if (e == cudaSuccess) e = launch_ce_finish(a, workspace, loss, lse, (cudaStream_t)stream);
@@ -910,7 +922,7 @@ int qamw_cross_entropy_grad(const void *X, int64_t T, int64_t K, int64_t ldx, co
   int rc;
   if (!lse || !grad_loss || !dX) return fail(QAMW_ENULL, "%s: lse, grad_loss and dX must be non-NULL", fn);
   CeArgsIn a{X, T, K, ldx, W, V, ldw, 0, V, targets, ignore_index, status};
-  if ((rc = check_ce_piece(a, fn))) return rc;
+  if ((rc = check_ce_piece(a, fn)) || (rc = check_vectors({lse, grad_loss}, 4, fn))) return rc;
   if (piece < 1 || piece > (int64_t(1) << 30) || (piece < V && piece % QAMW_VOCAB_TILE))
     return fail(QAMW_EINVAL, "%s: piece (%lld) must be a positive multiple of %d, or at least V", fn, (long long)piece,
                 QAMW_VOCAB_TILE);
