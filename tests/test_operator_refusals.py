@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import vector_codebook_codec_b200 as qamw
-from test_abi_host import (ODD, QAMW_EINVAL, _cef, _ceg, _cew, _cgw, _mxd, _mxl, _mxq)
+from test_abi_host import (FAKE, ODD, QAMW_EINVAL, QAMW_EUNSUPPORTED, _cef, _ceg, _cep, _cew, _cgw, _mxd, _mxl, _mxq)
 
 
 @pytest.fixture
@@ -59,4 +59,13 @@ def test_stream_of_another_device():
 def test_misaligned_vectors(lib, call, argument):
     """A float or int64 vector off its element's alignment would be a misaligned access on the GPU."""
     assert call(lib, **{argument: ODD}) == QAMW_EINVAL
+    assert lib.qamw_last_error()
+
+
+@pytest.mark.parametrize("call,kw", [(_cep, dict(ldx=1 << 39)), (_cep, dict(ldw=1 << 39)), (_cew, dict(ldw=1 << 39)),
+                                     (_cew, dict(ldx=1 << 39)), (_ceg, dict(ldw=1 << 39)), (_cgw, dict(ldw=1 << 39)),
+                                     (_cgw, dict(dW=FAKE, lddw=1 << 39)), (_ceg, dict(dW=FAKE, lddw=1 << 39))])
+def test_rows_further_apart_than_a_tensor_map_holds(lib, call, kw):
+    """Strides of 2^40 bytes: refused as arguments, before the kernels that need no tensor map are launched."""
+    assert call(lib, **kw) == QAMW_EUNSUPPORTED
     assert lib.qamw_last_error()

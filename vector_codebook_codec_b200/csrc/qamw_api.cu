@@ -792,6 +792,11 @@ static int check_ce_sizes(int64_t T, int64_t K, int64_t V, const char *fn) {
   return QAMW_OK;
 }
 
+// A tensor map holds strides below 2^40 bytes.
+static int check_ce_pitch(int64_t ld, const char *fn) {
+  return ld >= (int64_t(1) << 39) ? fail(QAMW_EUNSUPPORTED, "%s: rows too far apart (%lld)", fn, (long long)ld) : QAMW_OK;
+}
+
 static int check_ce_piece(const CeArgsIn &a, const char *fn) {
   int rc;
   if (!a.X || !a.W || !a.targets) return fail(QAMW_ENULL, "%s: X, W and targets must be non-NULL", fn);
@@ -805,6 +810,7 @@ static int check_ce_piece(const CeArgsIn &a, const char *fn) {
   if (a.ldx < a.K || a.ldw < a.K || a.ldx % 8 || a.ldw % 8)
     return fail(QAMW_EINVAL, "%s: ldx (%lld) and ldw (%lld) must be multiples of 8 and >= K", fn, (long long)a.ldx,
                 (long long)a.ldw);
+  if ((rc = check_ce_pitch(a.ldx, fn)) || (rc = check_ce_pitch(a.ldw, fn))) return rc;
   if (reinterpret_cast<uintptr_t>(a.X) % 16 || reinterpret_cast<uintptr_t>(a.W) % 16)
     return fail(QAMW_EINVAL, "%s: X and W must be 16-byte aligned", fn);
   return check_vectors({a.targets}, 8, fn);
@@ -875,6 +881,7 @@ int qamw_cross_entropy_grad_piece(const void *X, int64_t T, int64_t K, int64_t l
     return fail(QAMW_EINVAL, "%s: piece (%lld) must be at least n (%lld)", fn, (long long)piece, (long long)n);
   if (dW != nullptr && (lddw < K || reinterpret_cast<uintptr_t>(dW) % 2))
     return fail(QAMW_EINVAL, "%s: lddw (%lld) must be >= K and dW 2-byte aligned", fn, (long long)lddw);
+  if (dW != nullptr && (rc = check_ce_pitch(lddw, fn))) return rc;
   if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_grad_workspace(T, K, piece).total, fn))) return rc;
   cudaError_t e = launch_ce_grad_piece(a, lse, grad_loss, piece, first != 0, dW, lddw, workspace, (cudaStream_t)stream);
   return e == cudaSuccess ? QAMW_OK : cuda_fail(e, fn);
@@ -930,6 +937,7 @@ int qamw_cross_entropy_grad(const void *X, int64_t T, int64_t K, int64_t ldx, co
     return fail(QAMW_EINVAL, "%s: lddx (%lld) must be >= K and dX 2-byte aligned", fn, (long long)lddx);
   if (dW != nullptr && (lddw < K || reinterpret_cast<uintptr_t>(dW) % 2))
     return fail(QAMW_EINVAL, "%s: lddw (%lld) must be >= K and dW 2-byte aligned", fn, (long long)lddw);
+  if (dW != nullptr && (rc = check_ce_pitch(lddw, fn))) return rc;
   if ((rc = check_ce_workspace(workspace, workspace_bytes, ce_grad_workspace(T, K, piece).total, fn))) return rc;
   for (int64_t v0 = 0; v0 < V; v0 += piece) {
     a.v0 = v0;
