@@ -487,7 +487,8 @@ size_t qamw_mx4_linear_workspace_bytes(int64_t T, int64_t K);
  * [T][lddx]).
  *   lse : from the forward pass   grad_loss : device float32 [T], g_t = dL/dloss_t
  *   dW  : device bf16 [n][lddw], this piece's rows, or NULL (a frozen head)
- * G of a piece is rounded to bf16 (2^-8 relative at most) for the two products;
+ * G of a piece is rounded to bf16 (2^-8 relative at most) for the two products,
+ * or held as two bf16 terms (2^-16) for up to 16 tokens;
  * dX is summed over pieces and splits in fp32 in a fixed order and rounded once,
  * dW is rounded once. Rows of X whose token is ignored are not read into dW:
  * they may hold anything. Workspace: qamw_cross_entropy_grad_workspace_bytes(T,

@@ -1,6 +1,6 @@
 """The head's cross entropy and its gradient at the ends of what they take:
 tokens that the model is sure of, logits near the largest fp32 number, targets
-out of range, and the same call again.
+out of range, gradients of a few tokens, and the same call again.
 
 Logits here are products of one term, so they are exact. A loss is
 (max - l_target) + log(sum): the difference of two logits, rounded once
@@ -15,9 +15,10 @@ import pytest
 import torch
 
 import vector_codebook_codec_b200 as qamw
-from test_gpu_cross_entropy import _case, _coded_heads
+from test_gpu_cross_entropy import _case, _coded_heads, _forward64
 
 pytestmark = pytest.mark.gpu
+IGNORE = -100
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -107,6 +108,48 @@ def test_gradient_reports_targets_out_of_range():
     t[3] = 501
     qamw.cross_entropy_grad(X, mx, t, lse, g, piece=256, status=status)
     assert status.item() == qamw.STATUS_BAD_INDEX
+
+
+@pytest.mark.parametrize("T,K,V", [(1, 64, 500), (1, 2048, 1504), (2, 512, 3000), (3, 72, 257), (5, 1024, 4100), (7, 256, 777),
+                                   (16, 200, 1000), (16, 136, 2049)])
+@pytest.mark.parametrize("piece", [None, 256])
+def test_gradient_of_few_tokens_is_rounded_once(T, K, V, piece):
+    """With few tokens the rounding of G does not average out: up to 16 of them G is held to 2^-16 (two bf16
+    terms), and the outputs are rounded once. Logits wide enough that target probabilities spread over (0, 1).
+    The bounds are those of test_gpu_cross_entropy.py with 2^-16 |G| in place of 2^-8 |G|."""
+    X, W, t, g = _case(T, K, V, T + K + V, std=3.0 / K ** 0.5)
+    with torch.no_grad():                      # the target's logit among the largest
+        z = X.double() @ W.double().t()
+        t = torch.where(t == IGNORE, t, z.topk(3, dim=1).indices[:, 1])
+    _, lse = qamw.cross_entropy(X, W, t)
+    dX, dW = qamw.cross_entropy_grad(X, W, t, lse, g, piece=piece)
+    z, lse64, _, live, E = _forward64(X, W, t)
+    p = torch.exp(z - lse64[:, None])
+    G = p.clone()
+    G.scatter_add_(1, t.clamp(min=0)[:, None], -live.double()[:, None])
+    gl = torch.where(live, g.double(), torch.zeros_like(lse64))[:, None]
+    G = G * gl
+    dG = gl.abs() * (p * (E + (lse.double() - lse64).abs() + 2.0 ** -20)[:, None] + 2.0 ** -23) + 2.0 ** -16 * G.abs()
+    X64, W64 = X.double(), W.double()
+    for got, ref, tol in (
+            (dX, G @ W64, dG @ W64.abs() + (V / 16 + 2) * 2.0 ** -22 * (G.abs() @ W64.abs())),
+            (dW, G.t() @ X64, dG.t() @ X64.abs() + (T / 8 + 3) * 2.0 ** -22 * (G.abs().t() @ X64.abs()))):
+        assert ((got.double() - ref).abs() <= tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()).all()
+    assert (dX[~live] == 0).all()
+
+
+def test_gradient_of_few_tokens_with_an_infinite_weight():
+    """An infinite g_t: its own entries are Inf or NaN, the other tokens' rows of dX are what they were."""
+    X, W, t, g = _case(20, 64, 300, 18, ignored=0.0)
+    _, lse = qamw.cross_entropy(X, W, t)
+    g[7] = float("inf")
+    dX, _ = qamw.cross_entropy_grad(X, W, t, lse, g)
+    g[7] = 0
+    ref, _ = qamw.cross_entropy_grad(X, W, t, lse, g)
+    assert not torch.isfinite(dX[7]).any()
+    # their G is not scaled by max |g| then: other roundings
+    rest = torch.arange(20, device="cuda") != 7
+    assert ((dX - ref)[rest].abs().double() <= 2.0 ** -7 * ref[rest].abs().double() + 2.0 ** -15 * W.abs().sum(0).double()).all()
 
 
 @pytest.mark.parametrize("T,V,K", [(1, 1000, 256), (16, 3001, 1024), (301, 5021, 512), (700, 9000, 1024)])

@@ -15,8 +15,9 @@
 // where they are: the forward pass reduces 128 logits of a token to their
 // maximum and sum of exponentials (8 bytes leave the SM instead of 512), the
 // backward pass turns them into G. G of one piece is the only matrix of
-// that size that exists, rounded to bf16 once (2^-8 relative at most): bf16 is
-// the operand type that W and X have, and one tcgen05 product takes one type.
+// that size that exists, rounded to bf16 once (2^-8 relative at most; two terms
+// for few tokens, see kTwoTerms): bf16 is the operand type that W and X have,
+// and one tcgen05 product takes one type.
 //
 // A tile is 256 rows x 256 columns for a pair of CTAs (cta_group::2, 128
 // accumulator rows each; every CTA loads half of both operands), or 128 x 256
@@ -46,7 +47,7 @@ constexpr int kMaxStages = 8;
 constexpr int kShortDepth = 256;  // contraction up to which bf16 outputs leave by TMA stores (see run())
 constexpr int kGroupRows = 16;    // row tiles walked together (their operand stays in L2)
 
-enum Epilogue { kStats = 0, kGrad = 1, kStore = 2, kSlot = 3 };
+enum Epilogue { kStats = 0, kGrad = 1, kGradTwo = 2, kStore = 3, kSlot = 4 };   // kGradTwo: kGrad, two terms
 
 struct CeArgs {
   int64_t rows, cols, depth;      // of the product: D[rows][cols], contraction over depth
@@ -56,14 +57,14 @@ struct CeArgs {
   int stages;
   int a_bytes;                    // of a stage's row operand: rows x 128
   int32_t *status;
-  // kStats, kGrad: rows are tokens, columns the vocabulary entries v0 ..
+  // kStats, kGrad, kGradTwo: rows are tokens, columns the vocabulary entries v0 ..
   const int64_t *targets;         // [T]
   int64_t v0, V, ignore;
   float2 *partials;               // kStats: [half tiles of the whole vocabulary][T] (maximum, sum relative to it)
   float *target_logit;            // kStats: [T]
-  const float *lse, *grad;        // kGrad: [T]
-  const float *factor;            // kGrad: of G (divided out); kStore: of D
-  __nv_bfloat16 *out;             // kGrad: G, kStore: D
+  const float *lse, *grad;        // kGrad, kGradTwo: [T]
+  const float *factor;            // kGrad, kGradTwo: of G (divided out); kStore: of D
+  __nv_bfloat16 *out;             // kGrad: G, kGradTwo: its terms below one another, kStore: D
   int64_t ldo;
   int tma_out;                    // they leave by TMA stores
   float *slots;                   // kSlot: [splits][rows][cols] fp32
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                    const __grid_constant__ CUtensorMap omap, CeArgs g) {
   using L = CeTile<CTAS>;
+  constexpr bool kIsGrad = EPI == kGrad || EPI == kGradTwo;
   tc::griddep_launch_dependents();   // the next kernel may set up; it waits for this one before it reads or writes
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
@@ -290,12 +292,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY;                 // kStats
       float2 sum = make_float2(0.0f, 0.0f);   // of even and odd columns
       float lse = 0.0f, gr = 0.0f;         // kGrad
-      if constexpr (EPI == kStats || EPI == kGrad) {
+      if constexpr (EPI == kStats || kIsGrad) {
         const int64_t t = in ? g.targets[row] : g.ignore;
         const bool live = t != g.ignore && t >= 0 && t < g.V;
         const int64_t off = t - (g.v0 + col0);
         if (live && off >= 0 && off < n_cols) tcol = (int)off;
-        if constexpr (EPI == kGrad) {
+        if constexpr (kIsGrad) {
           lse = in ? g.lse[row] : 0.0f;
           gr = live ? __fdiv_rn(g.grad[row], *g.factor) : 0.0f;
         }
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 d = log2_ratio(v[j], v[j + 1], ref);
             sum = add2(sum, make_float2(exp2f(d.x), exp2f(d.y)));
           }
-        } else if constexpr (EPI == kGrad) {
+        } else if constexpr (kIsGrad) {
           const bool none = gr == 0.0f;
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
@@ -359,7 +361,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= scale;
         }
-        if constexpr (EPI == kGrad || EPI == kStore) {
+        if constexpr (EPI == kGradTwo) {
+          if (in) {
+            __nv_bfloat16 *o = g.out + row * g.ldo + col0 + c;
+            tc::store_row32(o, n, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float rest = v[j] - __bfloat162float(__float2bfloat16_rn(v[j]));
+              v[j] = fabsf(rest) < INFINITY ? rest : 0.0f;
+            }
+            tc::store_row32(o + g.rows * g.ldo, n, v);
+          }
+        } else if constexpr (EPI == kGrad || EPI == kStore) {
           if (g.tma_out) {
             if ((q & 1) == 0) {
               if (lane == 0) tc::stores_read();
@@ -469,8 +482,8 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const float2 
 // G^T X would still turn an Inf or NaN of a padded row into NaN.
 __global__ void __launch_bounds__(256) ce_prepare_kernel(const uint4 *X, int64_t ldx8, const int64_t *targets,
                                                          const float *grad, int64_t T, int64_t K8, int64_t V,
-                                                         int64_t ignore, uint4 *live, float *factor,
-                                                         int32_t *status) {
+                                                         int64_t ignore, int64_t rows, int64_t lo, uint4 *live,
+                                                         float *factor, int32_t *status) {
   tc::griddep_launch_dependents();
   auto counts = [&](int64_t t) {
     const int64_t at = targets[t];
@@ -494,24 +507,44 @@ __global__ void __launch_bounds__(256) ce_prepare_kernel(const uint4 *X, int64_t
     }
     return;
   }
-  for (int64_t i = (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x; i < T * K8; i += (int64_t)(gridDim.x - 1) * 256) {
-    const int64_t t = i / K8;
-    live[i] = counts(t) ? X[t * ldx8 + (i - t * K8)] : make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t i = (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x; i < rows * K8; i += (int64_t)(gridDim.x - 1) * 256) {
+    const int64_t r = i / K8, t = lo > 0 && r >= lo ? r - lo : r;
+    live[i] = t < T && counts(t) ? X[t * ldx8 + (i - r * K8)] : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
-// dX = the sum of the slots, in order, times the factor of G, rounded to bf16
-// (four columns a thread)
-__global__ void __launch_bounds__(256) ce_sum_slots_kernel(const float *slots, int splits, const float *factor,
-                                                           int64_t T, int64_t K, __nv_bfloat16 *dX, int64_t ldx) {
+// dX = the sum of its terms (`rows` rows apart) times the factor of G, rounded
+// to bf16, four columns a thread. GROUPS threads share the terms of a column,
+// each every GROUPS-th in order, and the first adds theirs in order: few tokens
+// have many terms and few columns (16 x 2048, 36 terms: 11.6 us with one thread
+// a column).
+template <int GROUPS>
+__global__ void __launch_bounds__(256) ce_sum_slots_kernel(const float *slots, int terms, int64_t rows,
+                                                           const float *factor, int64_t T, int64_t K,
+                                                           __nv_bfloat16 *dX, int64_t ldx) {
+  constexpr int kCols = 256 / GROUPS;
+  __shared__ float4 part[GROUPS][kCols];
+  const int c = threadIdx.x % kCols, group = threadIdx.x / kCols;
   const int64_t n = T * K / 4;
   const float f = *factor;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    float4 a = reinterpret_cast<const float4 *>(slots)[i];
-    for (int s = 1; s < splits; ++s) {
-      const float4 b = reinterpret_cast<const float4 *>(slots + (int64_t)s * T * K)[i];
-      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+  for (int64_t i0 = (int64_t)blockIdx.x * kCols; i0 < n; i0 += (int64_t)gridDim.x * kCols) {
+    const int64_t i = i0 + c;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float4 &b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; };
+    if (i < n) {
+#pragma unroll 8
+      for (int s = group; s < terms; s += GROUPS) add(reinterpret_cast<const float4 *>(slots + s * rows * K)[i]);
     }
+    if constexpr (GROUPS > 1) {
+      part[group][c] = a;
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int g = 1; g < GROUPS; ++g) add(part[g][c]);
+      }
+      __syncthreads();
+    }
+    if (group != 0 || i >= n) continue;
     const int64_t row = 4 * i / K, col = 4 * i - row * K;
     __nv_bfloat16 *o = dX + row * ldx + col;
     const __nv_bfloat162 p = __floats2bfloat162_rn(a.x * f, a.y * f), q = __floats2bfloat162_rn(a.z * f, a.w * f);
@@ -641,14 +674,26 @@ CeWorkspace ce_workspace(int64_t T, int64_t V) {
   return w;
 }
 
+// Up to 16 tokens G is held as two bf16 terms, rows t and lo + t of a matrix of
+// 2 lo rows: the tiles have room for both, so the products cost no more MMAs.
+// With so few tokens the rounding of one term would show: gradients were off by
+// up to 0.57% (one token) and by 1.9 times what their bf16 outputs cannot avoid.
+// From 17 tokens on it averages out (1.25 times at most in 12 thousand random
+// cases). 32000 x 2048, dX and dW / dX alone: 1 token 96 / 52 us (one term 95 /
+// 50), 16 tokens 94 / 55 (96 / 51); at 64 tokens two terms took 107 / 68 us, one
+// 94 / 56.
+constexpr int64_t kTwoTerms = 16;
+
 CeGradWorkspace ce_grad_workspace(int64_t T, int64_t K, int64_t piece) {
   CeGradWorkspace w;
   w.ldg = (piece + 7) / 8 * 8;
-  w.live = align256((size_t)T * (size_t)w.ldg * 2);
-  w.factor = w.live + align256((size_t)T * (size_t)K * 2);
+  w.lo = T <= kTwoTerms ? T : 0;
+  w.rows = T + w.lo;
+  w.live = align256((size_t)w.rows * (size_t)w.ldg * 2);
+  w.factor = w.live + align256((size_t)w.rows * (size_t)K * 2);
   w.slots = w.factor + 256;
-  w.splits = dx_splits(T, K, piece);
-  w.total = w.slots + align256((size_t)w.splits * (size_t)T * (size_t)K * 4);
+  w.splits = dx_splits(w.rows, K, piece);
+  w.total = w.slots + align256((size_t)w.splits * (size_t)w.rows * (size_t)K * 4);
   return w;
 }
 
@@ -693,14 +738,14 @@ cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const floa
   uint4 *live = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(workspace) + w.live);
   float *factor = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + w.factor);
   if (first) {
-    const int64_t blocks = (a.T * a.K / 8 + 255) / 256, most = (int64_t)sm_count() * 16;
+    const int64_t blocks = (w.rows * a.K / 8 + 255) / 256, most = (int64_t)sm_count() * 16;
     ce_prepare_kernel<<<(unsigned)(1 + std::min(blocks, most)), 256, 0, s>>>(
-        static_cast<const uint4 *>(a.X), a.ldx / 8, a.targets, grad, a.T, a.K / 8, a.V, a.ignore, live, factor,
-        a.status);
+        static_cast<const uint4 *>(a.X), a.ldx / 8, a.targets, grad, a.T, a.K / 8, a.V, a.ignore, w.rows,
+        w.lo, live, factor, a.status);
     const cudaError_t c = cudaGetLastError();
     if (c != cudaSuccess) return c;
   }
-  const Operand X{live, a.T, a.K, a.K};
+  const Operand X{live, w.rows, a.K, a.K}, Gm{G, w.rows, a.n, w.ldg};
   CeArgs g = {};
   g.rows = a.T;
   g.cols = a.n;
@@ -717,10 +762,11 @@ cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const floa
   g.factor = factor;
   g.out = G;
   g.ldo = w.ldg;
-  cudaError_t e = run_rows<false, false, kGrad>(X, {a.W, a.n, a.K, a.ldw}, g, s);
+  const Operand W{a.W, a.n, a.K, a.ldw};
+  cudaError_t e = w.lo > 0 ? run_rows<false, false, kGradTwo>(X, W, g, s) : run_rows<false, false, kGrad>(X, W, g, s);
   if (e != cudaSuccess) return e;
   CeArgs x = {};
-  x.rows = a.T;
+  x.rows = w.rows;
   x.cols = a.K;
   x.depth = a.n;
   x.splits = w.splits;
@@ -728,28 +774,36 @@ cudaError_t launch_ce_grad_piece(const CeArgsIn &a, const float *lse, const floa
   x.status = a.status;
   x.slots = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + w.slots);
   x.add = first ? 0 : 1;
-  if ((e = run_rows<false, true, kSlot>({G, a.T, a.n, w.ldg}, {a.W, a.n, a.K, a.ldw}, x, s)) != cudaSuccess) return e;
+  if ((e = run_rows<false, true, kSlot>(Gm, W, x, s)) != cudaSuccess) return e;
   if (dW == nullptr) return cudaSuccess;
   CeArgs d = {};
   d.rows = a.n;
   d.cols = a.K;
-  d.depth = a.T;
+  d.depth = w.rows;
   d.splits = 1;
-  d.steps_per_split = (a.T + kBK - 1) / kBK;
+  d.steps_per_split = (w.rows + kBK - 1) / kBK;
   d.status = a.status;
   d.factor = factor;
   d.out = static_cast<__nv_bfloat16 *>(dW);
   d.ldo = lddw;
-  return run_rows<true, true, kStore>({G, a.T, a.n, w.ldg}, X, d, s);
+  return run_rows<true, true, kStore>(Gm, X, d, s);
 }
 
 cudaError_t launch_ce_grad_finish(int64_t T, int64_t K, int64_t piece, void *dX, int64_t lddx, void *workspace,
                                   cudaStream_t s) {
   const CeGradWorkspace w = ce_grad_workspace(T, K, piece);
-  const int64_t blocks = (T * K / 4 + 255) / 256, most = (int64_t)sm_count() * 16;
-  ce_sum_slots_kernel<<<(unsigned)std::min(blocks, most), 256, 0, s>>>(
-      reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.slots), w.splits,
-      reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.factor), T, K, static_cast<__nv_bfloat16 *>(dX), lddx);
+  const int terms = w.lo > 0 ? 2 * w.splits : w.splits;
+  // one thread a column while that gives every SM a block (64 x 4096, 9 terms: 189 us of gradient, 193 shared)
+  const int groups = terms >= 8 && T * K / 4 < 256 * (int64_t)sm_count() ? 8 : 1;
+  const int64_t blocks = (T * K / 4 * groups + 255) / 256, most = (int64_t)sm_count() * 16;
+  auto run = [&](auto kernel) {
+    kernel<<<(unsigned)std::min(blocks, most), 256, 0, s>>>(
+        reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.slots), terms, w.lo > 0 ? w.lo : T,
+        reinterpret_cast<const float *>(static_cast<unsigned char *>(workspace) + w.factor), T, K,
+        static_cast<__nv_bfloat16 *>(dX), lddx);
+  };
+  if (groups == 8) run(ce_sum_slots_kernel<8>);
+  else run(ce_sum_slots_kernel<1>);
   return cudaGetLastError();
 }
 

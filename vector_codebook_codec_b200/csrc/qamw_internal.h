@@ -239,8 +239,10 @@ struct CeWorkspace {       // tile maxima and sums, then the targets' logits [T]
 CeWorkspace ce_workspace(int64_t T, int64_t V);
 cudaError_t launch_ce_piece(const CeArgsIn &a, void *workspace, cudaStream_t s);
 cudaError_t launch_ce_finish(const CeArgsIn &a, void *workspace, float *loss, float *lse, cudaStream_t s);
-struct CeGradWorkspace {   // G / factor bf16 [T][ldg], X without its ignored rows bf16 [T][K], the factor, the fp32
-  int64_t ldg;             // slots of dX [splits][T][K]
+// G / factor bf16 [rows][ldg], X without its ignored rows bf16 [rows][K], the factor, the fp32 slots of dX
+// [splits][rows][K]. rows = T; where G is held as two terms 2 T, token t's in rows t and lo + t (lo = T, else 0).
+struct CeGradWorkspace {
+  int64_t ldg, rows, lo;
   size_t live, factor, slots, total;
   int splits;
 };
