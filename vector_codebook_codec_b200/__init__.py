@@ -551,10 +551,11 @@ def _switched(device, stream):
 def _on(device, stream):
     """``device`` as the current one and ``stream`` as its current stream, so
     that what a call allocates for itself belongs to the stream that uses it."""
-    if stream is not None and stream.device != device:
+    if stream is None:
+        if device.index == _torch()._C._cuda_getDevice():
+            return _NULL_CONTEXT
+    elif stream.device != device:
         raise ValueError(f"stream must be on {device}, got {stream.device}")
-    if stream is None and device.index == _torch()._C._cuda_getDevice():
-        return _NULL_CONTEXT
     return _switched(device, stream)
 
 
@@ -880,7 +881,9 @@ def cross_entropy(X, head, targets, codebook=None, ignore_index: int = -100, pie
     head, without keeping the logits: returns (loss, lse), float32 [T] each.
     ``head`` is a bf16 tensor [V, K], an :class:`Encoded` matrix (with its
     ``codebook``) or an :class:`Mx4`; coded heads are decoded to bf16 ``piece``
-    rows at a time. ``targets`` is int64 [T]; ``ignore_index`` has loss 0."""
+    rows at a time. ``targets`` is int64 [T]; ``ignore_index`` has loss 0. The
+    results are no part of an autograd graph: the gradients are a call of their
+    own, :func:`cross_entropy_grad`."""
     torch = _torch()
     h, ldx, device = _ce_inputs(X, head, targets, codebook, status)
     T, K, V, lib = X.shape[0], h.K, h.V, load_library()
