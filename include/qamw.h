@@ -473,8 +473,9 @@ size_t qamw_mx4_linear_workspace_bytes(int64_t T, int64_t K);
  *   X : device bf16 [T][ldx]    W : device bf16 [n][ldw]   (16-byte aligned,
  *       ldx and ldw multiples of 8; K a multiple of 8, T at most 2^24)
  *   targets : device int64 [T]  workspace : device, 256-byte aligned
- * Products of bf16 values with fp32 accumulation (tcgen05), softmax statistics
- * in fp32. A timed-out wait sets QAMW_STATUS_TIMEOUT.
+ * Products of bf16 values with fp32 accumulation (tcgen05, whose sums are cut
+ * off, not rounded, below their last bit: lse is off by about 8e-7 of itself at
+ * K = 4096), softmax statistics in fp32. A timed-out wait sets QAMW_STATUS_TIMEOUT.
  *
  * Forward: qamw_cross_entropy_piece for every piece (in any order, one
  * stream), then qamw_cross_entropy_finish writes loss and lse (device float32

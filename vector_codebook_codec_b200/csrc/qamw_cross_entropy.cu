@@ -25,10 +25,14 @@
 // the MMAs fill the other.
 //
 // Bound by power for large products: 4096 tokens x 32000 x 4096 forward takes
-// 0.645 ms in a burst (1.66 PFLOP/s) and 0.77 ms back to back, the gradient of
-// 4096 x 65536 x 4096 4.4 and 5.0 ms (1.5 and 1.32 PFLOP/s over its three
-// products). For few tokens by the read of W: 16 x 32000 x 2048 takes 30 us,
-// 4.4 TB/s with its start and finish, 16 x 32000 x 8192 6 TB/s.
+// 0.64 ms in a run of 20 calls (1.68 PFLOP/s) and 0.78 ms back to back, the
+// gradient of 4096 x 65536 x 4096 4.2 and 4.9 ms (1.57 and 1.35 PFLOP/s over its
+// three products). For few tokens by the read of W: 16 x 32000 x 2048 takes 30 us,
+// 4.4 TB/s with its start and finish, 16 x 32000 x 8192 88 us, 5.9 TB/s.
+//
+// The tensor cores add in fp32 and cut off what lies below the sum's last bit, so
+// logits are off by about K / 16 x 2^-24 of their size: lse of 4096 columns by
+// 7.6e-7 of itself (with rounding 8e-8), a loss by some 1e-5.
 #include <algorithm>
 
 #include "qamw_device.cuh"

@@ -42,7 +42,8 @@ namespace {
 
 constexpr int kMxWarps = 4;         // warps per CTA
 // Warps that an SM is meant to hold: 16 (128 registers) for the quantisation of
-// prepared rows (11008 x 4096 bf16, b = 128: 71 us; 20 warps the same, 24 spill: 84),
+// prepared rows (11008 x 4096 bf16, b = 128, before its rows were taken in turn: 71 us,
+// 20 warps the same, 24 spill: 84),
 // and for decoding rotated ones, 24 for the kernels that neither bound an error
 // nor rotate (values of the same matrix decoded: 29 us at 16, 27 at 24).
 constexpr int kMxResident = 16, kMxResidentPlain = 24;
@@ -335,10 +336,10 @@ __device__ __forceinline__ void rotate(float2 (&x)[16], int lane) {
 }
 
 // PREP: a channel scale or a rotation (blocks of 2^LB columns); otherwise the
-// values are exact as read. 11008 x 4096 bf16: 62 us at b = 128 with a scale
-// (1.8 TB/s; 760 instructions per 1024 values, 240 of them on the integer pipe
-// at half rate, 16 warps per SM; 66 us with the rows dealt out beforehand), 23
-// us plain (5 TB/s).
+// values are exact as read. 11008 x 4096 bf16: 60 us at b = 128 with a scale
+// (1.9 TB/s; 784 instructions per 1024 values, 245 of them on the integer pipe at
+// half rate, 14 warps per SM, 60% of the issue slots; 66 us with the rows dealt
+// out beforehand), 23 us plain (5 TB/s).
 template <typename T, bool PREP, int LB>
 __global__ void __launch_bounds__(32 * kMxWarps, (PREP ? kMxResident : kMxResidentPlain) / kMxWarps)
     mx4_quantize_kernel(const __grid_constant__ MxQuantArgs p) {
@@ -616,9 +617,11 @@ __device__ __noinline__ void decode_exactly(const MxDecodeArgs &p, bool every) {
 // they hold in the quantisation. Block bits 0-4 stay inside a group, whose
 // values share a scale: their sums (at most 32 x 6, in halves) are exact in
 // fp16, two columns an instruction and two an exchange between lanes. Then the
-// scale, and the other bits in fp32. What bounds the kernel is the exchanges:
-// 5120 x 13824 at b = 256 took 59 us with all bits in fp32 and the factors in
-// shared memory (L1 pipe 81% busy).
+// scale, and the other bits in fp32. 11008 x 4096 bf16 at b = 128: 33 us (3.5
+// TB/s), 5120 x 13824 at b = 256: 52 us (with all bits in fp32 and the factors in
+// shared memory 59, its L1 pipe 81% busy; now 62%, at b = 128 49%). No pipe is
+// full: 13 warps per SM issue in 57-60% of the slots, and wait for fixed
+// latencies and for the next row's loads.
 template <typename T, int LB>
 __global__ void __launch_bounds__(32 * kMxWarps, (LB > 0 ? kMxResident : kMxResidentPlain) / kMxWarps)
     mx4_decode_kernel(const __grid_constant__ MxDecodeArgs p) {

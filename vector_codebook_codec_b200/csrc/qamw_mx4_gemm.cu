@@ -12,14 +12,16 @@
 //  - up to 128 tokens: a CTA's tile is 128 weight rows (the tensor-memory
 //    lanes) by NT tokens; the weights are all there is to read, so the columns
 //    are split over a cluster until the SMs are busy, and the parts are added
-//    in shared memory in the order of the ranks. 37 tokens x 13824 x 5120: 11 us
-//    (3.5 TB/s with its start and end), 1 token x 4096 x 4096: 5 us;
+//    in shared memory in the order of the ranks. The kernel alone (one after
+//    another in a graph, other weights each time): 37 tokens x 13824 x 5120 12 us
+//    (3.1 TB/s with its start and end), 128 tokens 13, 1 token x 4096 x 4096 6 us;
 //  - more tokens: a pair of CTAs (cta_group::2) takes 256 tokens x 256 weight
 //    rows, persistent. A token is a lane, so its outputs are contiguous. 4096
-//    tokens x 11008 x 4096: 78 us (4.7 PFLOP/s), x 16384 columns: 93 us (5.9);
-//    a step's MMAs take 594 of 512 nominal cycles whether or not anything is
-//    loaded, and the accumulator's drain 1.3 of 13 thousand cycles a tile: two
-//    of 256 columns and the scales do not fit tensor memory together.
+//    tokens x 11008 x 4096: 76 us (4.9 PFLOP/s), 4096 x 4096 x 16384: 105 us back to
+//    back (5.3); a step's MMAs take 594 of 512 nominal cycles whether or not
+//    anything is loaded, and the accumulator's drain 1.3 of 13 thousand cycles a
+//    tile: two accumulators of 256 columns and the scales do not fit tensor memory
+//    together (two of 192 would; not tried).
 #include <algorithm>
 
 #include "qamw_device.cuh"
@@ -496,9 +498,9 @@ cudaError_t run_split(const Mx4MatmulArgs &a, MxGemmArgs g, int smem_max, cudaSt
     return cudaErrorInvalidValue;
   // Splits: the power of two that minimises waves x (steps of a CTA + 4, the
   // steps' worth of a CTA's start and end). One CTA per SM with all its memory:
-  // two with half of it, and twice the splits, were slower (37 tokens x 13824 x
-  // 5120: 16 us, 22 in halves; 128 tokens: 18 and 37, most of it for adding the
-  // parts).
+  // two with half of it, and twice the splits, were slower (whole calls then: 37
+  // tokens x 13824 x 5120 16 us, in halves 22; 128 tokens 18 and 37, most of it for
+  // adding the parts).
   const int64_t tiles = (a.M + 127) / 128, steps = (a.K + kBK - 1) / kBK;
   int64_t best = INT64_MAX;
   for (int sp = 1; sp <= 8 && sp <= steps; sp *= 2) {
