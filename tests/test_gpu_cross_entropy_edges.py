@@ -168,3 +168,58 @@ def test_the_same_call_gives_the_same_bits(T, V, K):
         torch.cuda.synchronize()
         for r in (got[0], got[2]):
             assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
+@pytest.mark.parametrize("T", [1, 9, 16, 17])
+def test_few_tokens_in_every_form(T):
+    """Around the border of the two-term gradient: coded heads by pieces, slices of wider matrices, a replayed graph."""
+    V, K = 900, 256
+    enc, C, mx = _coded_heads(V, K, T)
+    X, _, t, g = _case(T, K, V, 80 + T)
+    W = qamw.mx4_decode(mx)
+    for head, cb, rows in ((enc, C, qamw.decode(enc, C)), (mx, None, W)):
+        for piece in (None, 256):
+            _, lse = qamw.cross_entropy(X, head, t, codebook=cb, piece=piece)
+            got = qamw.cross_entropy_grad(X, head, t, lse, g, codebook=cb, piece=piece, weight_grad=True)
+            want = qamw.cross_entropy_grad(X, rows, t, lse, g, piece=piece)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    wide = torch.full((T, K + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:8 + K] = X
+    got = qamw.cross_entropy_grad(wide[:, 8:8 + K], W, t, lse, g)
+    want = qamw.cross_entropy_grad(X, W, t, lse, g)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dX, dW = qamw.cross_entropy_grad(X, W, t, lse, g)
+    for seed in (1, 2):
+        Y, _, u, h = _case(T, K, V, 90 + seed)
+        X.copy_(Y), t.copy_(u), g.copy_(h)
+        lse.copy_(qamw.cross_entropy(X, W, t)[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = qamw.cross_entropy_grad(X, W, t, lse, g)
+        assert torch.equal(dX, want[0]) and torch.equal(dW, want[1])
+
+
+def test_few_and_many_tokens_on_two_streams():
+    """Two-term and one-term gradients and decodes that need fp64, at once."""
+    a, b = _case(11, 512, 3000, 91), _case(200, 256, 2000, 92)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    big = qamw.mx4_quantize(torch.randn((300, 1024), device="cuda").clamp(-3, 3) * 2.0 ** 124, 64, 1)
+    want = []
+    for X, W, t, g in (a, b):
+        loss, lse = qamw.cross_entropy(X, W, t)
+        want.append((loss, lse) + qamw.cross_entropy_grad(X, W, t, lse, g))
+    decoded = qamw.mx4_decode(big)
+    assert torch.isfinite(decoded).all()
+    torch.cuda.synchronize()
+    got, ds = [[], []], []
+    for _ in range(10):
+        for n, (X, W, t, g) in enumerate((a, b)):
+            loss, lse = qamw.cross_entropy(X, W, t, stream=streams[n])
+            got[n].append((loss, lse) + qamw.cross_entropy_grad(X, W, t, lse, g, stream=streams[n]))
+        ds.append(qamw.mx4_decode(big, stream=streams[2]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for n in range(2) for r in got[n] for p, q in zip(r, want[n]))
+    assert all(torch.equal(d, decoded) for d in ds)
